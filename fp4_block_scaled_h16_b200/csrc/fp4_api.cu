@@ -661,6 +661,198 @@ fp4_status_t fp4_gemm(fp4_format_t format, int double_block,
     return FP4_OK;
 }
 
+// ------------------------------------------------------------------ FP8 with a scale per block of 128
+
+size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines) {
+    if (lines <= 0 || K <= 0 || (block_lines != 1 && block_lines != 128)) return 0;
+    return (size_t)((K + 127) / 128) * (size_t)fp8_scale_lines(lines, block_lines);
+}
+
+// sizes that the kernels' 32-bit tile coordinates hold
+static bool fits32(int64_t n) { return n <= 0x7fffffff - 512; }
+
+fp4_status_t fp4_fp8_block_quantize(const void* x, fp4_in_dtype_t in_dtype, int64_t rows, int64_t cols, int64_t ld,
+                                    int block_lines, uint8_t* codes_rows, int64_t ld_rows, float* scales_rows,
+                                    uint8_t* codes_cols, int64_t ld_cols, float* scales_cols, void* stream) {
+    fp4_status_t st = check_input(x, in_dtype, rows, cols, ld, FP4_ROT_NONE, 1);
+    if (st != FP4_OK) return st;
+    if (block_lines != 1 && block_lines != 128) return FP4_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return FP4_OK;
+    if (!codes_rows && !codes_cols) return FP4_ERR_INVALID_ARG;
+    if ((codes_rows && (!scales_rows || ld_rows < cols)) || (codes_cols && (!scales_cols || ld_cols < rows)))
+        return FP4_ERR_INVALID_ARG;
+    if ((codes_rows && (!aligned16(codes_rows) || !aligned16(scales_rows) || ld_rows % 16)) ||
+        (codes_cols && (!aligned16(codes_cols) || !aligned16(scales_cols) || ld_cols % 16)))
+        return FP4_ERR_MISALIGNED;
+    if (!fits32(rows) || !fits32(cols) || ((rows + 127) / 128) * ((cols + 127) / 128) > 0x7fffffff)
+        return FP4_ERR_UNSUPPORTED_SHAPE;
+    int dev;
+    if ((st = device_ready(&dev)) != FP4_OK) return st;
+    Fp8QuantArgs a{};
+    a.x = x; a.bf16 = in_dtype == FP4_IN_BF16;
+    a.rows = rows; a.cols = cols; a.ld = ld;
+    a.block_lines = block_lines;
+    a.codes_rows = codes_rows; a.ld_rows = ld_rows; a.scales_rows = scales_rows;
+    a.codes_cols = codes_cols; a.ld_cols = ld_cols; a.scales_cols = scales_cols;
+    a.wait_limit = g_wait_limit;
+    if (launch_fp8_quantize(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP4_ERR_CUDA;
+    return FP4_OK;
+}
+
+fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float* a_scales, const uint8_t* b_codes,
+                                int64_t ldb, const float* b_scales, int b_block_lines, int64_t M, int64_t N, int64_t K,
+                                void* c, fp4_out_dtype_t out_dtype, int64_t ldc, void* stream) {
+    if (out_dtype != FP4_OUT_F32 && out_dtype != FP4_OUT_BF16) return FP4_ERR_INVALID_ARG;
+    if (b_block_lines != 1 && b_block_lines != 128) return FP4_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || ldc < N || lda < K || ldb < K) return FP4_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return FP4_OK;
+    if (K == 0 || !fits32(M) || !fits32(N) || !fits32(K)) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return FP4_ERR_INVALID_ARG;
+    const int64_t es = out_dtype == FP4_OUT_BF16 ? 2 : 4;
+    if (!aligned16(a_codes) || !aligned16(b_codes) || !aligned16(a_scales) || !aligned16(b_scales) || !aligned16(c) ||
+        lda % 16 || ldb % 16 || (ldc * es) % 16)
+        return FP4_ERR_MISALIGNED;
+    int dev;
+    fp4_status_t st;
+    if ((st = device_ready(&dev)) != FP4_OK) return st;
+    Fp8GemmArgs g{};
+    g.a_codes = a_codes; g.lda = lda; g.a_scales = a_scales;
+    g.b_codes = b_codes; g.ldb = ldb; g.b_scales = b_scales;
+    g.b_lines = b_block_lines;
+    g.M = M; g.N = N; g.K = K; g.c = c; g.ldc = ldc;
+    g.out_bf16 = out_dtype == FP4_OUT_BF16;
+    g.wait_limit = g_wait_limit;
+    // pair tiles once they occupy half of the SM pairs and are not mostly padding
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool pairs = g_gemm_pairs && M > 128 && gemm_fp8_pair_tiles(M, N) * 4 >= num_sms();
+    if ((pairs ? launch_gemm_fp8_pair(g, s) : launch_gemm_fp8_split(g, s)) != cudaSuccess) return FP4_ERR_CUDA;
+    return FP4_OK;
+}
+
+// ------------------------------------------------------------------ norms, gate and residual
+
+// a [.., ld] matrix of `es`-byte elements that a kernel reads or writes 16 bytes at a time
+static fp4_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int64_t es) {
+    if (ld < cols) return FP4_ERR_INVALID_ARG;
+    return (!aligned16(p) || (ld * es) % 16) ? FP4_ERR_MISALIGNED : FP4_OK;
+}
+
+fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_t ldh, fp4_in_dtype_t dtype,
+                               int64_t rows, int64_t cols, const void* w_post, const void* gate, int64_t ld_gate,
+                               int64_t rows_per_group, float alpha, const void* w_pre, float eps, void* h_out,
+                               int64_t ld_hout, void* y, int64_t ldy, uint8_t* codes, int64_t ld_codes, float* scales,
+                               float* rstd_post, float* rstd_pre, void* stream) {
+    if (dtype != FP4_IN_F32 && dtype != FP4_IN_BF16) return FP4_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 0) return FP4_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f && eps <= 3.4028234663852886e38f) || !(alpha - alpha == 0.0f)) return FP4_ERR_INVALID_ARG;
+    if (gate && rows_per_group < 1) return FP4_ERR_INVALID_ARG;
+    if (cols > 16384) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0 || cols == 0) return FP4_OK;      // empty tensors may have null pointers
+    if ((w_post || gate) && !o) return FP4_ERR_INVALID_ARG;
+    if ((w_pre != nullptr) != (y || codes) || (!o && !w_pre)) return FP4_ERR_INVALID_ARG;
+    if (!h || (o && !h_out) || (w_post && !rstd_post) || (w_pre && !rstd_pre) || (codes && !scales))
+        return FP4_ERR_INVALID_ARG;
+    const int64_t es = dtype == FP4_IN_BF16 ? 2 : 4;
+    fp4_status_t st = check_matrix(h, ldh, cols, es);
+    if (st == FP4_OK && o) st = check_matrix(o, ldo, cols, es);
+    if (st == FP4_OK && o) st = check_matrix(h_out, ld_hout, cols, es);
+    if (st == FP4_OK && gate) st = check_matrix(gate, ld_gate, cols, es);
+    if (st == FP4_OK && y) st = check_matrix(y, ldy, cols, es);
+    if (st == FP4_OK && codes) st = check_matrix(codes, ld_codes, cols, 1);
+    if (st != FP4_OK) return st;
+    if (!aligned16(w_post) || !aligned16(w_pre) || !aligned16(scales) || ((uintptr_t)rstd_post & 3u) ||
+        ((uintptr_t)rstd_pre & 3u))
+        return FP4_ERR_MISALIGNED;
+    int dev;
+    if ((st = device_ready(&dev)) != FP4_OK) return st;
+    NormArgs a{};
+    a.o = o; a.ldo = ldo; a.h = h; a.ldh = ldh;
+    a.rows = rows; a.cols = cols;
+    a.w_post = w_post; a.gate = gate; a.ldg = ld_gate; a.per = rows_per_group;
+    a.alpha = alpha; a.eps = eps; a.w_pre = w_pre;
+    a.h_out = h_out; a.ldho = ld_hout; a.y = y; a.ldy = ldy;
+    a.codes = codes; a.ldc = ld_codes; a.lp = fp8_scale_lines(rows, 1); a.scales = scales;
+    a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+    if (launch_norm(a, dtype == FP4_IN_BF16, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FP4_ERR_CUDA;
+    return FP4_OK;
+}
+
+fp4_status_t fp4_norm_residual_backward_workspace_size(int64_t rows, int64_t cols, int has_pre, int has_post,
+                                                       int has_gate, int64_t rows_per_group, size_t* bytes) {
+    if (!bytes || rows < 0 || cols < 0 || (has_gate && rows_per_group < 1)) return FP4_ERR_INVALID_ARG;
+    if (cols > 16384) return FP4_ERR_UNSUPPORTED_SHAPE;
+    *bytes = 0;
+    if (rows == 0 || cols == 0) return FP4_OK;
+    static const char some = 0;
+    NormBwdArgs a{};
+    a.rows = rows; a.cols = cols;
+    a.w_pre = has_pre ? &some : nullptr;
+    a.w_post = has_post ? &some : nullptr;
+    a.gate = has_gate ? &some : nullptr;
+    a.per = rows_per_group;
+    norm_bwd_plan(a);
+    *bytes = norm_bwd_workspace(a);
+    return FP4_OK;
+}
+
+fp4_status_t fp4_norm_residual_backward(const void* dy, int64_t lddy, const void* dh_in, int64_t ld_dhin,
+                                        const void* h, int64_t ldh, const void* o, int64_t ldo, fp4_in_dtype_t dtype,
+                                        int64_t rows, int64_t cols, const void* w_post, const void* gate,
+                                        int64_t ld_gate, int64_t rows_per_group, float alpha, const void* w_pre,
+                                        const float* rstd_post, const float* rstd_pre, void* dh, int64_t ld_dh,
+                                        void* d_o, int64_t ld_do, float* dw_pre, float* dw_post, float* dgate,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    if (dtype != FP4_IN_F32 && dtype != FP4_IN_BF16) return FP4_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 0 || !(alpha - alpha == 0.0f)) return FP4_ERR_INVALID_ARG;
+    if ((w_pre != nullptr) != (dw_pre != nullptr) || (w_post != nullptr) != (dw_post != nullptr) ||
+        (gate != nullptr) != (dgate != nullptr) || ((w_post || gate) && !d_o && rows > 0 && cols > 0))
+        return FP4_ERR_INVALID_ARG;
+    if (gate && rows_per_group < 1) return FP4_ERR_INVALID_ARG;
+    if (cols > 16384) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (((uintptr_t)dw_pre & 15u) || ((uintptr_t)dw_post & 15u) || !aligned16(dgate)) return FP4_ERR_MISALIGNED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int dev;
+    fp4_status_t st;
+    if (rows == 0 || cols == 0) {            // empty sums
+        if (cols == 0 || (!dw_pre && !dw_post)) return FP4_OK;
+        if ((st = device_ready(&dev)) != FP4_OK) return st;
+        if ((dw_pre && cudaMemsetAsync(dw_pre, 0, (size_t)cols * 4, s) != cudaSuccess) ||
+            (dw_post && cudaMemsetAsync(dw_post, 0, (size_t)cols * 4, s) != cudaSuccess))
+            return FP4_ERR_CUDA;
+        return FP4_OK;
+    }
+    if ((w_pre != nullptr) != (dy != nullptr) || (w_pre && (!h || !rstd_pre)) || (!dy && !dh_in) || !dh)
+        return FP4_ERR_INVALID_ARG;
+    if ((o != nullptr) != (d_o != nullptr) || (w_post && !rstd_post)) return FP4_ERR_INVALID_ARG;
+    const int64_t es = dtype == FP4_IN_BF16 ? 2 : 4;
+    st = check_matrix(dh, ld_dh, cols, es);
+    if (st == FP4_OK && dy) st = check_matrix(dy, lddy, cols, es);
+    if (st == FP4_OK && dh_in) st = check_matrix(dh_in, ld_dhin, cols, es);
+    if (st == FP4_OK && w_pre) st = check_matrix(h, ldh, cols, es);
+    if (st == FP4_OK && o) st = check_matrix(o, ldo, cols, es);
+    if (st == FP4_OK && o) st = check_matrix(d_o, ld_do, cols, es);
+    if (st == FP4_OK && gate) st = check_matrix(gate, ld_gate, cols, es);
+    if (st != FP4_OK) return st;
+    if (!aligned16(w_post) || !aligned16(w_pre) || ((uintptr_t)rstd_post & 3u) || ((uintptr_t)rstd_pre & 3u))
+        return FP4_ERR_MISALIGNED;
+    NormBwdArgs a{};
+    a.dy = dy; a.lddy = lddy; a.dh_in = dh_in; a.lddhi = ld_dhin; a.h = h; a.ldh = ldh; a.o = o; a.ldo = ldo;
+    a.rows = rows; a.cols = cols;
+    a.w_post = w_post; a.gate = gate; a.ldg = ld_gate; a.per = rows_per_group; a.alpha = alpha; a.w_pre = w_pre;
+    a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+    a.dh = dh; a.lddh = ld_dh; a.d_o = d_o; a.lddo = ld_do;
+    a.dw_pre = dw_pre; a.dw_post = dw_post; a.dgate = dgate;
+    norm_bwd_plan(a);
+    const size_t need = norm_bwd_workspace(a);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return FP4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return FP4_ERR_MISALIGNED;
+    }
+    if ((st = device_ready(&dev)) != FP4_OK) return st;
+    if (launch_norm_bwd(a, dtype == FP4_IN_BF16, static_cast<float*>(workspace), s) != cudaSuccess) return FP4_ERR_CUDA;
+    return FP4_OK;
+}
+
 fp4_status_t fp4_last_error(void* stream) {
     int dev;
     fp4_status_t st;

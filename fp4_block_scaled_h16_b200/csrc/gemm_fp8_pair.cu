@@ -1,0 +1,447 @@
+// gemm_fp8_pair.cu -- the FP8 block-scaled GEMM (fp4_fp8_block_gemm) for
+// outputs large enough to fill the GPU with 256 x 256 tiles:
+//
+//   C[i, j] = sum_kc sA[kc, i] sB[kc, j or j / 128] P_kc[i, j],
+//   P_kc[i, j] = sum_{k in chunk kc of 128} qA[i, k] qB[j, k].
+//
+// An FP32 scale per 128-K chunk cannot ride in the tensor core's accumulator,
+// so every chunk is a partial product of its own, promoted in binary32
+// registers: acc += sA (sB P).  The partial of a chunk is 256 x 256 over a CTA
+// pair (tcgen05.mma cta_group::2 kind::f8f6f4, four of K = 32), 128 x 256 per
+// CTA: 256 TMEM columns, so all 512 columns hold two partials and the tensor
+// core fills one while eight warps promote the other.  Per SM a chunk is 512
+// tensor cycles; its promotion is 32768 multiply-adds, 256 cycles of the FP32
+// pipe (512 when B's scales differ per line), and 128 KB of TMEM reads, 256
+// cycles: it hides behind the tensor core with 128 x 128 blocks of B, and is
+// about level with it with 1 x 128 blocks.
+//
+// Roles (both CTAs, 384 threads, persistent over pair tiles, one CTA per SM):
+//   warp 0   TMA producer: this CTA's 128 rows of A and 128 lines of B per
+//            chunk (counted on the leader's barrier), and, on a ring of its
+//            own, the chunk's scales of its rows (and of the tile's columns);
+//   warp 1   TMEM; in the leader one thread issues both CTAs' MMAs;
+//   warps 4-11  promotion, 32 rows x 128 columns each (128 accumulators and a
+//            32-column slice per thread; setmaxnreg moves the registers of
+//            warps 0-3 here), then the output: 32-row x 128-byte boxes in
+//            swizzled shared memory and TMA stores.
+// No load uses cluster multicast.  Every wait is bounded; one that runs out
+// sets the device error word to FP4_ERR_TIMEOUT, and before either CTA exits
+// the leader settles every load either CTA issued, as in gemm_pair.cu.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace fp4 {
+
+namespace {
+
+constexpr int PM = 256, PN = 256;        // tile of a CTA pair
+constexpr int BK = 128;                  // K elements (bytes) per stage: one scale chunk
+constexpr int NUM_THREADS = 384;
+constexpr int PROMO_WARPS = 8;
+constexpr int STAGES = 5;
+constexpr int SC_SLOTS = 8;              // ring of scale slots
+constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK;
+constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t SC_BYTES = 128 * 4 + PN * 4;      // scales of 128 rows and of 256 columns
+constexpr uint32_t EPI_BUF = 4096;       // per promotion warp: one 32-row x 128-byte box of C
+constexpr uint32_t SMEM = STAGES * STAGE_BYTES + PROMO_WARPS * EPI_BUF + SC_SLOTS * SC_BYTES + 512 + 1024;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t DRAIN_LIMIT = 1u << 22;
+constexpr unsigned int ERR_TIMEOUT = 7u;
+static_assert(SMEM <= 232448u, "shared memory");
+
+struct PairParams {
+    const float* sa;          // [chunks, lpa]
+    const float* sb;          // [chunks, lpb]
+    int64_t lpa, lpb;
+    void* c;
+    int64_t ldc;
+    int M, N, chunks;
+    int odd_n;                // N ends inside a 16-byte chunk of a row of C
+    int tiles_m, tiles_n;
+    uint32_t wait_limit;
+    unsigned int* err;
+};
+
+__device__ __forceinline__ void raise_timeout(const PairParams& p, volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicExch(p.err, ERR_TIMEOUT);
+}
+
+// M = 256 E4M3 MMA over the pair: rows 0-127 of A and D in the leader, 128-255
+// in the peer; B's first 128 lines from the leader's shared memory, the rest
+// from the peer's
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u)
+                 : "memory");
+}
+
+// VEC: B's scales are one per line (1 x 128 blocks), else one per 128 lines
+template <bool VEC, bool OUT_BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmC, const PairParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte aligned base, at the same offset in both CTAs
+    const uint32_t raw = sm100::smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint8_t* epi_bufs = smem + STAGES * STAGE_BYTES;
+    uint8_t* sc_ring = epi_bufs + PROMO_WARPS * EPI_BUF;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sc_ring + SC_SLOTS * SC_BYTES);
+    uint64_t* empty = full + STAGES;
+    uint64_t* sfull = empty + STAGES;
+    uint64_t* sempty = sfull + SC_SLOTS;
+    uint64_t* pfull = sempty + SC_SLOTS;
+    uint64_t* pempty = pfull + 2;
+    uint64_t* drain = pempty + 2;
+    uint64_t* peer_done = drain + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* peer_fills = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = sm100::cluster_rank();
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int tiles = p.tiles_m * p.tiles_n;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            sm100::mbar_init(&full[s], 1);
+            sm100::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < SC_SLOTS; ++s) {
+            sm100::mbar_init(&sfull[s], 1);
+            sm100::mbar_init(&sempty[s], PROMO_WARPS);
+        }
+        for (int b = 0; b < 2; ++b) {
+            sm100::mbar_init(&pfull[b], 1);
+            sm100::mbar_init(&pempty[b], 2 * PROMO_WARPS);
+        }
+        sm100::mbar_init(drain, 1);
+        sm100::mbar_init(peer_done, 1);
+        *abort_flag = 0;
+        *peer_fills = 0;
+        sm100::fence_barrier_init();
+        sm100::prefetch_tmap(&tmA);
+        sm100::prefetch_tmap(&tmB);
+        sm100::prefetch_tmap(&tmC);
+    }
+    if (warp == 1) {
+        sm100::tmem_alloc_pair(tmem_slot, TMEM_COLS);
+        sm100::tmem_relinquish_pair();
+    }
+    sm100::tc_fence_before();
+    sm100::cluster_sync();        // both CTAs' barriers initialised before any load signals them
+    sm100::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        // 384 threads x 168 registers at launch = 128 x 40 + 256 x 232
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            // -------------------------------------------------------- producer
+            if (sm100::elect_one()) {
+                int stage = 0, slot = 0;
+                uint32_t phase = 0, sphase = 0;
+                uint32_t fills = 0, sfills = 0;
+                bool ok = true;
+                for (int u = pair; u < tiles && ok; u += pairs) {
+                    int tm_, tn_;
+                    tile_coords(u, p.tiles_m, p.tiles_n, tm_, tn_);
+                    const int n0 = tn_ * PN;
+                    const int ma = tm_ * PM + 128 * (int)rank;       // this CTA's rows of A
+                    const int nb = n0 + 128 * (int)rank;             // ... and lines of B
+                    // scale bytes that exist: scale rows are padded to 128 lines
+                    const uint32_t sa_bytes = ma < p.lpa ? 512u : 0u;
+                    const uint32_t sb_bytes = !VEC ? 0u : (n0 + 128 < p.lpb ? 1024u : 512u);
+                    for (int kc = 0; kc < p.chunks; ++kc) {
+                        if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, p.wait_limit, abort_flag) ||
+                            !sm100::mbar_wait(&sempty[slot], sphase ^ 1u, p.wait_limit, abort_flag)) {
+                            raise_timeout(p, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* st = smem + stage * STAGE_BYTES;
+                        const uint32_t bar = sm100::cluster_addr(&full[stage], 0);
+                        if (rank == 0) sm100::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
+                        sm100::tma_load_2d_pair(st, &tmA, kc * BK, ma, bar);
+                        sm100::tma_load_2d_pair(st + A_BYTES, &tmB, kc * BK, nb, bar);
+                        ++fills;
+                        uint8_t* sc = sc_ring + slot * SC_BYTES;
+                        sm100::mbar_arrive_expect_tx(&sfull[slot], sa_bytes + sb_bytes);
+                        if (sa_bytes) sm100::bulk_load(sc, p.sa + kc * p.lpa + ma, sa_bytes, &sfull[slot]);
+                        if (VEC) sm100::bulk_load(sc + 512, p.sb + kc * p.lpb + n0, sb_bytes, &sfull[slot]);
+                        ++sfills;
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                        if (++slot == SC_SLOTS) { slot = 0; sphase ^= 1u; }
+                    }
+                }
+                for (int s = 0; s < SC_SLOTS; ++s)
+                    if (sfills > (uint32_t)s)
+                        sm100::mbar_wait(&sfull[s], ((sfills - 1u - s) / SC_SLOTS) & 1u, DRAIN_LIMIT, nullptr);
+                if (rank == 1) {
+                    // report the fills to the leader, whose barriers count their bytes
+                    sm100::st_cluster_u32(sm100::cluster_addr(const_cast<uint32_t*>(peer_fills), 0), fills);
+                    sm100::mbar_arrive_cluster(sm100::cluster_addr(peer_done, 0));
+                } else {
+                    // after a timeout the two producers may have filled different
+                    // numbers of stages: complete the bookkeeping of every fill
+                    // either CTA issued, then wait for the last phase of each stage
+                    uint32_t pf = fills;
+                    if (sm100::mbar_wait_cluster(peer_done, 0, DRAIN_LIMIT, nullptr)) pf = *peer_fills;
+                    else raise_timeout(p, abort_flag);
+                    const uint32_t lf = fills;
+                    for (uint32_t i = lf; i < pf; ++i) {          // the peer's half only: expect it
+                        const uint32_t s = i % STAGES;
+                        if (i >= (uint32_t)STAGES)
+                            sm100::mbar_wait(&full[s], ((i - STAGES) / STAGES) & 1u, DRAIN_LIMIT, nullptr);
+                        sm100::mbar_arrive_expect_tx(&full[s], STAGE_BYTES);
+                    }
+                    for (uint32_t i = pf; i < lf; ++i) {          // this CTA's half only: the peer's never comes
+                        const uint32_t s = i % STAGES;
+                        if (i >= (uint32_t)STAGES)
+                            sm100::mbar_wait(&full[s], ((i - STAGES) / STAGES) & 1u, DRAIN_LIMIT, nullptr);
+                        sm100::mbar_complete_tx(&full[s], STAGE_BYTES);
+                    }
+                    const uint32_t last = lf > pf ? lf : pf;
+                    for (int s = 0; s < STAGES; ++s)
+                        if (last > (uint32_t)s)
+                            sm100::mbar_wait(&full[s], ((last - 1u - s) / STAGES) & 1u, DRAIN_LIMIT, nullptr);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------------------------------------- MMA issuer (leader)
+            if (rank == 0 && sm100::elect_one()) {
+                int stage = 0, pb = 0;
+                uint32_t phase = 0, pphase = 0;
+                bool ok = true, issued = false;
+                constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+                for (int u = pair; u < tiles && ok; u += pairs) {
+                    for (int kc = 0; kc < p.chunks; ++kc) {
+                        if (!sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag) ||
+                            !sm100::mbar_wait(&pempty[pb], pphase ^ 1u, p.wait_limit, abort_flag)) {
+                            raise_timeout(p, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        sm100::tc_fence_after();
+                        const uint32_t st = sm100::smem_u32(smem + stage * STAGE_BYTES);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 32; ++kk)
+                            mma_f8_pair(tmem + PN * pb, sm100::desc_sw128(st + 32 * kk),
+                                        sm100::desc_sw128(st + A_BYTES + 32 * kk), idesc, kk > 0 ? 1u : 0u);
+                        issued = true;
+                        sm100::tc_commit_pair_both(&empty[stage]);   // both CTAs' stage free
+                        sm100::tc_commit_pair_both(&pfull[pb]);      // both halves of the partial ready
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                        pb ^= 1;
+                        if (pb == 0) pphase ^= 1u;
+                    }
+                }
+                if (issued) {
+                    sm100::tc_commit_pair_local(drain);
+                    sm100::mbar_wait(drain, 0, DRAIN_LIMIT, nullptr);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        // ------------------------------------------------------------ promotion and output
+        constexpr int COLS = PN / 2;                    // columns per warp
+        constexpr int BOX_COLS = OUT_BF16 ? 64 : 32;    // 128 bytes of a row of C
+        const int q = warp & 3;                         // TMEM lane quarter of this warp
+        const int half = (warp - 4) >> 2;               // which half of the tile's columns
+        uint8_t* buf = epi_bufs + (warp - 4) * EPI_BUF;
+        const uint32_t buf_s = sm100::smem_u32(buf);
+        const uint32_t leader_pempty = sm100::cluster_addr(pempty, 0);
+        int slot = 0, pb = 0;
+        uint32_t sphase = 0, pphase = 0;
+        bool ok = true;
+        for (int u = pair; u < tiles && ok; u += pairs) {
+            int tm_, tn_;
+            tile_coords(u, p.tiles_m, p.tiles_n, tm_, tn_);
+            const int n0 = tn_ * PN + half * COLS;
+            const int row0 = tm_ * PM + 128 * (int)rank + 32 * q;
+            // block scales of B: one value per chunk for this warp's 128 columns
+            // (columns past N take the last block's; they are not stored)
+            const int nblk = VEC ? 0 : min(n0 / 128, (int)p.lpb - 1);
+            float sb_next = VEC ? 0.0f : __ldg(p.sb + nblk);
+            float2 acc[COLS / 2];
+#pragma unroll
+            for (int c = 0; c < COLS / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            for (int kc = 0; kc < p.chunks; ++kc) {
+                const float sb = sb_next;
+                if (!VEC && kc + 1 < p.chunks) sb_next = __ldg(p.sb + (kc + 1) * p.lpb + nblk);
+                const bool got = sm100::mbar_wait(&sfull[slot], sphase, p.wait_limit, abort_flag) &&
+                                 sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    if (lane == 0) raise_timeout(p, abort_flag);
+                    ok = false;
+                    break;
+                }
+                sm100::tc_fence_after();
+                const float* sc = reinterpret_cast<const float*>(sc_ring + slot * SC_BYTES);
+                const float sa = sc[32 * q + lane];
+                const float s = VEC ? sa : __fmul_rn(sa, sb);
+                const float2 s2 = make_float2(s, s);
+                const float4* sbv = reinterpret_cast<const float4*>(sc + 128 + half * COLS);
+                const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + PN * pb + half * COLS;
+                // four slices of 32 columns: the next one's TMEM load is in
+                // flight while one is promoted
+                uint32_t r[2][32];
+                sm100::tmem_ld32(base, r[0]);
+#pragma unroll
+                for (int g = 0; g < COLS / 32; ++g) {
+                    sm100::tmem_ld_wait_on(r[g & 1]);
+                    if (g + 1 < COLS / 32) sm100::tmem_ld32(base + 32 * (g + 1), r[(g + 1) & 1]);
+                    else {
+                        sm100::tc_fence_before();
+                        __syncwarp();
+                        // the tensor core may refill this partial
+                        if (lane == 0) sm100::mbar_arrive_cluster_relaxed(leader_pempty + 8u * (uint32_t)pb);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float2 p0 = make_float2(__uint_as_float(r[g & 1][4 * c]), __uint_as_float(r[g & 1][4 * c + 1]));
+                        float2 p1 = make_float2(__uint_as_float(r[g & 1][4 * c + 2]), __uint_as_float(r[g & 1][4 * c + 3]));
+                        if (VEC) {
+                            const float4 w = sbv[8 * g + c];
+                            p0 = __fmul2_rn(p0, make_float2(w.x, w.y));
+                            p1 = __fmul2_rn(p1, make_float2(w.z, w.w));
+                        }
+                        acc[16 * g + 2 * c] = __ffma2_rn(p0, s2, acc[16 * g + 2 * c]);
+                        acc[16 * g + 2 * c + 1] = __ffma2_rn(p1, s2, acc[16 * g + 2 * c + 1]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(&sempty[slot]);
+                if (++slot == SC_SLOTS) { slot = 0; sphase ^= 1u; }
+                pb ^= 1;
+                if (pb == 0) pphase ^= 1u;
+            }
+            if (!ok) break;
+            // rows row0 .. row0 + 31 (lane = row), columns n0 .. n0 + 127
+#pragma unroll
+            for (int b = 0; b < COLS / BOX_COLS; ++b) {
+                if (p.odd_n && n0 + (b + 1) * BOX_COLS > p.N) {
+                    // a TMA store clips a row at 16 bytes, so a box in which C
+                    // ends inside a 16-byte chunk is written by the lanes
+                    if (row0 + lane < p.M) {
+#pragma unroll
+                        for (int e = 0; e < BOX_COLS; ++e) {
+                            const int i = b * BOX_COLS + e;
+                            const float v = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+                            const int64_t at = (int64_t)(row0 + lane) * p.ldc + n0 + i;
+                            if (n0 + i < p.N) {
+                                if (OUT_BF16) static_cast<__nv_bfloat16*>(p.c)[at] = __float2bfloat16_rn(v);
+                                else static_cast<float*>(p.c)[at] = v;
+                            }
+                        }
+                    }
+                    continue;
+                }
+                if (lane == 0) sm100::bulk_wait_read0();        // the previous box has left the buffer
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {                    // 16-byte chunk c of this lane's row
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (OUT_BF16) {
+                            const float2 v = acc[(b * BOX_COLS + 8 * c + 2 * e) / 2];
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        } else {
+                            const float2 v = acc[(b * BOX_COLS + 4 * c + e) / 2];
+                            w[e] = __float_as_uint((e & 1) ? v.y : v.x);
+                        }
+                    }
+                    sm100::st_shared_v4(buf_s + lane * 128 + ((c ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                }
+                sm100::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && row0 < p.M && n0 + b * BOX_COLS < p.N) {
+                    sm100::tma_store_2d(&tmC, buf, n0 + b * BOX_COLS, row0);
+                    sm100::bulk_commit();
+                }
+            }
+        }
+        if (lane == 0) sm100::bulk_wait0();     // this warp's stores are complete before the CTA leaves
+        __syncwarp();
+    }
+
+    // neither CTA frees its TMEM or leaves while the leader's MMAs or either
+    // CTA's loads may still touch it
+    sm100::tc_fence_before();
+    sm100::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        sm100::tc_fence_after();
+        sm100::tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
+template <bool VEC, bool OUT_BF16>
+cudaError_t run_pair(const Fp8GemmArgs& g, cudaStream_t s) {
+    static PerDeviceOnce setup;
+    static int max_pairs[kOnceDevices] = {};
+    int dev = 0;
+    const cudaError_t attr_err = setup.run([](int d) {
+        cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<VEC, OUT_BF16>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * 512);
+        cfg.blockDim = dim3(NUM_THREADS);
+        cfg.dynamicSmemBytes = SMEM;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_pair_kernel<VEC, OUT_BF16>, &cfg);
+        if (e != cudaSuccess) return e;
+        max_pairs[d] = n;
+        return n > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+    }, &dev);
+    if (attr_err != cudaSuccess) return attr_err;
+    CUtensorMap ta, tb, tc;
+    if (!make_fp8_map(&ta, g.a_codes, g.M, g.K, g.lda, 128) || !make_fp8_map(&tb, g.b_codes, g.N, g.K, g.ldb, 128) ||
+        !make_c_map(&tc, g.c, OUT_BF16, g.M, g.N, g.ldc))
+        return cudaErrorInvalidValue;
+    PairParams p{};
+    p.sa = g.a_scales;
+    p.sb = g.b_scales;
+    p.lpa = fp8_scale_lines(g.M, 1);
+    p.lpb = fp8_scale_lines(g.N, g.b_lines);
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.c = g.c;
+    p.ldc = g.ldc;
+    p.odd_n = (g.N * (OUT_BF16 ? 2 : 4)) % 16 != 0;
+    p.chunks = (int)((g.K + BK - 1) / BK);
+    p.tiles_m = (int)((g.M + PM - 1) / PM);
+    p.tiles_n = (int)((g.N + PN - 1) / PN);
+    p.wait_limit = g.wait_limit;
+    p.err = device_error_word();
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
+    gemm_fp8_pair_kernel<VEC, OUT_BF16><<<2 * pairs, NUM_THREADS, SMEM, s>>>(ta, tb, tc, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t gemm_fp8_pair_tiles(int64_t M, int64_t N) { return ((M + PM - 1) / PM) * ((N + PN - 1) / PN); }
+
+cudaError_t launch_gemm_fp8_pair(const Fp8GemmArgs& g, cudaStream_t s) {
+    if (g.b_lines == 1) return g.out_bf16 ? run_pair<true, true>(g, s) : run_pair<true, false>(g, s);
+    return g.out_bf16 ? run_pair<false, true>(g, s) : run_pair<false, false>(g, s);
+}
+
+}  // namespace fp4

@@ -163,6 +163,107 @@ bool make_c_map(CUtensorMap* m, void* c, bool bf16, int64_t M, int64_t N, int64_
 // the driver's cuTensorMapEncodeTiled (null when the driver has none)
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
+// FP8 with a scale per block of 128 along K (fp8_quantize.cu, gemm_fp8_*.cu).
+// Scales are [ceil(K / 128), fp8_scale_lines]: lines padded to 128 for 1 x 128
+// blocks, blocks of lines for 128 x 128 blocks.
+inline int64_t fp8_scale_lines(int64_t lines, int block_lines) {
+    return block_lines == 1 ? (lines + 127) / 128 * 128 : (lines + 127) / 128;
+}
+struct Fp8QuantArgs {
+    const void* x;
+    bool bf16;
+    int64_t rows, cols, ld;
+    int block_lines;
+    uint8_t* codes_rows;        // [rows, ld_rows], or null
+    int64_t ld_rows;
+    float* scales_rows;
+    uint8_t* codes_cols;        // [cols, ld_cols], or null
+    int64_t ld_cols;
+    float* scales_cols;
+    uint32_t wait_limit;
+};
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t s);
+// 2-D TMA map over E4M3 codes [lines, K] of row pitch `pitch`: box 128 bytes x
+// box_lines, 128-byte swizzle, zeros past the edges
+bool make_fp8_map(CUtensorMap* m, const uint8_t* codes, int64_t lines, int64_t K, int64_t pitch, int box_lines);
+struct Fp8GemmArgs {
+    const uint8_t* a_codes;     // [M, lda], 1 x 128 blocks
+    int64_t lda;
+    const float* a_scales;
+    const uint8_t* b_codes;     // [N, ldb], b_lines x 128 blocks
+    int64_t ldb;
+    const float* b_scales;
+    int b_lines;
+    int64_t M, N, K;
+    void* c;
+    int64_t ldc;
+    int out_bf16;
+    uint32_t wait_limit;
+};
+cudaError_t launch_gemm_fp8_split(const Fp8GemmArgs& g, cudaStream_t s);   // 128 lines x up to 128 rows, K over a cluster
+cudaError_t launch_gemm_fp8_pair(const Fp8GemmArgs& g, cudaStream_t s);    // 256 x 256 tiles on CTA pairs
+int64_t gemm_fp8_pair_tiles(int64_t M, int64_t N);
+
+// the norms around a block with its gate and residual update (norm_residual.cu);
+// null pointers select what is left out
+struct NormArgs {
+    const void* o;              // block output, or null: h' = h
+    int64_t ldo;
+    const void* h;
+    int64_t ldh;
+    int64_t rows, cols;
+    const void* w_post;         // [cols], or null: the block output is not normalised
+    const void* gate;           // [ceil(rows / per), ldg], or null
+    int64_t ldg, per;
+    float alpha, eps;
+    const void* w_pre;          // [cols], or null: no y
+    void* h_out;
+    int64_t ldho;
+    void* y;
+    int64_t ldy;
+    uint8_t* codes;             // y in E4M3 with 1 x 128 blocks, or null
+    int64_t ldc, lp;
+    float* scales;
+    float* rstd_post;
+    float* rstd_pre;
+};
+cudaError_t launch_norm(const NormArgs& a, bool bf16, cudaStream_t s);
+constexpr int NORM_BWD_CTAS = 296;   // two per SM of a B200: partial sums per column
+struct NormBwdArgs {
+    const void* dy;
+    int64_t lddy;
+    const void* dh_in;
+    int64_t lddhi;
+    const void* h;              // h' as stored by the forward call
+    int64_t ldh;
+    const void* o;
+    int64_t ldo;
+    int64_t rows, cols;
+    const void* w_post;
+    const void* gate;
+    int64_t ldg, per;
+    float alpha;
+    const void* w_pre;
+    const float* rstd_post;
+    const float* rstd_pre;
+    void* dh;
+    int64_t lddh;
+    void* d_o;
+    int64_t lddo;
+    float* dw_pre;
+    float* dw_post;
+    float* dgate;
+    // the plan (norm_bwd_plan): groups of `per` rows in nseg segments of
+    // seg_rows; items = groups * nseg
+    int64_t groups, nseg, seg_rows, items, pitch, gate_pitch;
+    float* pre_part;
+    float* post_part;
+    float* gate_part;
+};
+void norm_bwd_plan(NormBwdArgs& a);
+size_t norm_bwd_workspace(const NormBwdArgs& a);
+cudaError_t launch_norm_bwd(NormBwdArgs a, bool bf16, float* workspace, cudaStream_t s);
+
 // One-time setup per device (kernel attributes and occupancy are properties of
 // the kernel on one device): run() calls init once for the current device and
 // returns its cached status afterwards.

@@ -258,6 +258,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
+// the same without ordering this thread's memory accesses: for a hand-over of
+// TMEM, which tcgen05.fence orders (a release at cluster scope waits for every
+// access of the thread, over a microsecond in a promotion loop)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t caddr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
 // take `bytes` off the pending transaction count of a local mbarrier without arriving
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.complete_tx.shared::cluster.relaxed.cluster.b64 [%0], %1;"

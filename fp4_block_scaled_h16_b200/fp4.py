@@ -35,7 +35,9 @@ EXPORTS = ("fp4_scales_bytes", "fp4_quantize_workspace_size", "fp4_amax", "fp4_q
            "fp4_gemm", "fp4_last_error", "fp4_status_string", "fp4_set_wait_limit",
            "fp4_quantize_noalloc", "fp4_requantize", "fp4_rotate", "fp4_mxnorm_quantize",
            "fp4_gemm_workspace_size", "fp4_channel_amax", "fp4_outctl_workspace_size", "fp4_outctl_quantize",
-           "fp4_gemm_outctl", "fp4_set_gemm_cta_pairs", "fp4_quantize_both_axes")
+           "fp4_gemm_outctl", "fp4_set_gemm_cta_pairs", "fp4_quantize_both_axes", "fp4_fp8_block_scales_count",
+           "fp4_fp8_block_quantize", "fp4_fp8_block_gemm", "fp4_norm_residual",
+           "fp4_norm_residual_backward_workspace_size", "fp4_norm_residual_backward")
 
 _P, _I, _I64, _U64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
                                  ctypes.c_uint32, ctypes.c_size_t)
@@ -62,6 +64,16 @@ _lib.fp4_gemm_outctl.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _
 _lib.fp4_rotate.argtypes = [_P, _I, _I64, _I64, _I64, _I, _I, _U64, _P, _I64, _P]
 _lib.fp4_gemm.argtypes = [_I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]
 _lib.fp4_gemm_workspace_size.argtypes = [_I, _I, _I64, _I64, _I64, ctypes.POINTER(_SZ)]
+_F = ctypes.c_float
+_lib.fp4_fp8_block_scales_count.argtypes = [_I64, _I64, _I]
+_lib.fp4_fp8_block_scales_count.restype = _SZ
+_lib.fp4_fp8_block_quantize.argtypes = [_P, _I, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _I64, _P, _P]
+_lib.fp4_fp8_block_gemm.argtypes = [_P, _I64, _P, _P, _I64, _P, _I, _I64, _I64, _I64, _P, _I, _I64, _P]
+_lib.fp4_norm_residual.argtypes = [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _P, _I64, _I64, _F, _P, _F, _P, _I64, _P,
+                                   _I64, _P, _I64, _P, _P, _P, _P]
+_lib.fp4_norm_residual_backward_workspace_size.argtypes = [_I64, _I64, _I, _I, _I, _I64, ctypes.POINTER(_SZ)]
+_lib.fp4_norm_residual_backward.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I64, _I64, _P, _P, _I64, _I64,
+                                            _F, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]
 _lib.fp4_last_error.argtypes = [_P]
 _lib.fp4_set_wait_limit.argtypes = [_U32]
 _lib.fp4_set_wait_limit.restype = None
@@ -70,7 +82,8 @@ _lib.fp4_set_gemm_cta_pairs.restype = None
 for _f in ("fp4_amax", "fp4_rotate", "fp4_mxnorm_quantize", "fp4_gemm_workspace_size", "fp4_channel_amax",
            "fp4_outctl_workspace_size", "fp4_outctl_quantize", "fp4_gemm_outctl", "fp4_quantize", "fp4_quantize_noalloc",
            "fp4_quantize_both_axes", "fp4_requantize", "fp4_gemm", "fp4_last_error",
-           "fp4_quantize_workspace_size"):
+           "fp4_quantize_workspace_size", "fp4_fp8_block_quantize", "fp4_fp8_block_gemm", "fp4_norm_residual",
+           "fp4_norm_residual_backward_workspace_size", "fp4_norm_residual_backward"):
     getattr(_lib, _f).restype = _I
 
 
@@ -405,3 +418,288 @@ def gemm_outctl(qa, qb, out_dtype=FP4_OUT_F32, out=None, stream=None):
                     a8["codes"], a8["scale"], b8["codes"], b8["scale"], M, N, K, K8, out, out_dtype, out.stride(0),
                     stream)
     return out
+
+
+# --------------------------------------------------------------------------- FP8, a scale per block of 128
+
+def fp4_fp8_block_scales_count(lines: int, K: int, block_lines: int) -> int:
+    return _lib.fp4_fp8_block_scales_count(lines, K, block_lines)
+
+
+def fp4_fp8_block_quantize(x, in_dtype, rows, cols, ld, block_lines, codes_rows, ld_rows, scales_rows, codes_cols,
+                           ld_cols, scales_cols, stream=None) -> None:
+    _check(_lib.fp4_fp8_block_quantize(_ptr(x), in_dtype, rows, cols, ld, block_lines, _ptr(codes_rows), ld_rows,
+                                       _ptr(scales_rows), _ptr(codes_cols), ld_cols, _ptr(scales_cols),
+                                       _stream(stream)), "fp4_fp8_block_quantize")
+
+
+def fp4_fp8_block_gemm(a_codes, lda, a_scales, b_codes, ldb, b_scales, b_block_lines, M, N, K, c, out_dtype, ldc,
+                       stream=None) -> None:
+    _check(_lib.fp4_fp8_block_gemm(_ptr(a_codes), lda, _ptr(a_scales), _ptr(b_codes), ldb, _ptr(b_scales),
+                                   b_block_lines, M, N, K, _ptr(c), out_dtype, ldc, _stream(stream)),
+           "fp4_fp8_block_gemm")
+
+
+def _pitch(t) -> int:
+    """Row pitch in elements of a 2-D tensor with unit stride in its last dim."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _want(t, what: str, shape=None, dtype=None, like=None):
+    """Refuse a tensor that the call would read or write wrongly."""
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (what, shape, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.numel() and t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must have unit stride in its last dimension" % what)
+    if like is not None and t.device != like.device:
+        raise ValueError("%s is on %s, the other tensors on %s" % (what, t.device, like.device))
+
+
+def _on_current_device(t, what: str):
+    """The library launches on the current device; a tensor of another one is refused."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
+
+
+def alloc_fp8_block(lines: int, K: int, block_lines: int = 1, device="cuda"):
+    """E4M3 codes [lines, K rounded up to 16] u8 and scales [ceil(K / 128), ...] f32 (include/fp4.h)."""
+    import torch
+    if block_lines not in (1, 128):
+        raise ValueError("block_lines must be 1 or 128, got %r" % (block_lines,))
+    n = (lines + 127) // 128 * (128 if block_lines == 1 else 1)
+    return dict(codes=torch.empty((lines, (K + 15) // 16 * 16), dtype=torch.uint8, device=device),
+                scales=torch.empty(((K + 127) // 128, n), dtype=torch.float32, device=device),
+                lines=lines, K=K, block_lines=block_lines)
+
+
+def _fp8_tensor(q, what: str, lines: int, K: int, block_lines: int, like):
+    """Codes, their pitch and the scales of an FP8 tensor, checked."""
+    import torch
+    codes, scales = q["codes"], q["scales"]
+    if q["lines"] != lines or q["K"] != K or q["block_lines"] != block_lines:
+        raise ValueError("%s must hold %d lines of %d in blocks of %d lines" % (what, lines, K, block_lines))
+    if codes.dim() != 2 or codes.shape[0] != lines or codes.shape[1] < K:
+        raise ValueError("%s: codes must be [%d, >= %d], got %s" % (what, lines, K, tuple(codes.shape)))
+    _want(codes, what + " codes", dtype=torch.uint8, like=like)
+    n = (lines + 127) // 128 * (128 if block_lines == 1 else 1)
+    _want(scales, what + " scales", shape=((K + 127) // 128, n), dtype=torch.float32, like=like)
+    if not scales.is_contiguous():
+        raise ValueError("%s: scales must be contiguous" % what)
+    return codes, _pitch(codes), scales
+
+
+def _fp8_quantize(x, block_lines, rows_q, cols_q, stream):
+    rows, cols = x.shape
+    cr = _fp8_tensor(rows_q, "the rows' result", rows, cols, block_lines, x) if rows_q is not None else (None, 0, None)
+    cc = _fp8_tensor(cols_q, "the columns' result", cols, rows, block_lines, x) if cols_q is not None else (None, 0, None)
+    fp4_fp8_block_quantize(x, in_dtype_of(x), rows, cols, _pitch(x), block_lines, *cr, *cc, stream)
+
+
+def fp8_block_quantize(x, axis=1, block_lines=1, out=None, stream=None):
+    """E4M3 of a 2-D CUDA tensor with a scale per block of 128 along its rows
+    (axis 1) or its columns (axis 0: the transposed tensor), of block_lines (1
+    or 128) lines (fp4_fp8_block_quantize); into a new or given FP8 tensor
+    {"codes", "scales", "lines", "K", "block_lines"}."""
+    if axis not in (0, 1):
+        raise ValueError("axis must be 0 or 1, got %r" % (axis,))
+    _on_current_device(x, "x")
+    _want(x, "x")
+    rows, cols = x.shape
+    q = out if out is not None else alloc_fp8_block(*((rows, cols) if axis else (cols, rows)), block_lines, x.device)
+    _fp8_quantize(x, block_lines, q if axis else None, None if axis else q, stream)
+    return q
+
+
+def fp8_block_quantize_both_axes(x, block_lines=1, out_rows=None, out_cols=None, stream=None):
+    """fp8_block_quantize along the rows and along the columns from one read;
+    returns (FP8 tensor of the rows, FP8 tensor of the columns)."""
+    _on_current_device(x, "x")
+    _want(x, "x")
+    rows, cols = x.shape
+    qr = out_rows if out_rows is not None else alloc_fp8_block(rows, cols, block_lines, x.device)
+    qc = out_cols if out_cols is not None else alloc_fp8_block(cols, rows, block_lines, x.device)
+    _fp8_quantize(x, block_lines, qr, qc, stream)
+    return qr, qc
+
+
+def fp8_block_gemm(qa, qb, out_dtype=FP4_OUT_F32, out=None, stream=None):
+    """C = A B^T on two FP8 tensors (fp4_fp8_block_gemm): A in 1 x 128 blocks,
+    B in 1 x 128 or 128 x 128 blocks."""
+    import torch
+    M, N, K = qa["lines"], qb["lines"], qa["K"]
+    if qb["K"] != K or qa["block_lines"] != 1:
+        raise ValueError("operands must share K, and A must have 1 x 128 blocks")
+    _on_current_device(qa["codes"], "A")
+    a, lda, sa = _fp8_tensor(qa, "A", M, K, 1, qa["codes"])
+    b, ldb, sb = _fp8_tensor(qb, "B", N, K, qb["block_lines"], a)
+    dtype = torch.bfloat16 if out_dtype == FP4_OUT_BF16 else torch.float32
+    if out is None:
+        out = torch.empty((M, (N + 7) // 8 * 8), dtype=dtype, device=a.device)[:, :N]
+    else:
+        _want(out, "out", shape=(M, N), dtype=dtype, like=a)
+    fp4_fp8_block_gemm(a, lda, sa, b, ldb, sb, qb["block_lines"], M, N, K, out, out_dtype, _pitch(out), stream)
+    return out
+
+
+# --------------------------------------------------------------------------- norms, gate and residual
+
+def fp4_norm_residual(o, ldo, h, ldh, dtype, rows, cols, w_post, gate, ld_gate, rows_per_group, alpha, w_pre, eps,
+                      h_out, ld_hout, y, ldy, codes, ld_codes, scales, rstd_post, rstd_pre, stream=None) -> None:
+    _check(_lib.fp4_norm_residual(_ptr(o), ldo, _ptr(h), ldh, dtype, rows, cols, _ptr(w_post), _ptr(gate), ld_gate,
+                                  rows_per_group, alpha, _ptr(w_pre), eps, _ptr(h_out), ld_hout, _ptr(y), ldy,
+                                  _ptr(codes), ld_codes, _ptr(scales), _ptr(rstd_post), _ptr(rstd_pre),
+                                  _stream(stream)), "fp4_norm_residual")
+
+
+def fp4_norm_residual_backward_workspace_size(rows, cols, has_pre, has_post, has_gate, rows_per_group) -> int:
+    n = _SZ(0)
+    _check(_lib.fp4_norm_residual_backward_workspace_size(rows, cols, int(has_pre), int(has_post), int(has_gate),
+                                                          rows_per_group, ctypes.byref(n)),
+           "fp4_norm_residual_backward_workspace_size")
+    return n.value
+
+
+def fp4_norm_residual_backward(dy, lddy, dh_in, ld_dhin, h, ldh, o, ldo, dtype, rows, cols, w_post, gate, ld_gate,
+                               rows_per_group, alpha, w_pre, rstd_post, rstd_pre, dh, ld_dh, d_o, ld_do, dw_pre,
+                               dw_post, dgate, workspace, workspace_bytes, stream=None) -> None:
+    _check(_lib.fp4_norm_residual_backward(_ptr(dy), lddy, _ptr(dh_in), ld_dhin, _ptr(h), ldh, _ptr(o), ldo, dtype,
+                                           rows, cols, _ptr(w_post), _ptr(gate), ld_gate, rows_per_group, alpha,
+                                           _ptr(w_pre), _ptr(rstd_post), _ptr(rstd_pre), _ptr(dh), ld_dh, _ptr(d_o),
+                                           ld_do, _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), _ptr(workspace),
+                                           workspace_bytes, _stream(stream)), "fp4_norm_residual_backward")
+
+
+def _mat(t, what, shape, like):
+    """(tensor, row pitch) of an optional [rows, cols] tensor of like's type."""
+    if t is None:
+        return None, 0
+    _want(t, what, shape=shape, dtype=like.dtype, like=like)
+    return t, _pitch(t)
+
+
+def _gate_of(gate, rows_per_group, rows, cols, like):
+    if gate is None:
+        return None, 0, 0
+    if rows_per_group is None or rows_per_group < 1:
+        raise ValueError("a gate needs rows_per_group >= 1")
+    t, ld = _mat(gate, "gate", ((rows + rows_per_group - 1) // rows_per_group, cols), like)
+    return t, ld, rows_per_group
+
+
+def _float_vector(t, what, shape, like):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    _want(t, what, shape=shape, dtype=torch.float32, like=like)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t
+
+
+def _blank(like, rows, cols):
+    """A [rows, cols] tensor of like's type whose row pitch is a multiple of 16 bytes."""
+    import torch
+    return torch.empty((rows, (cols + 7) // 8 * 8), dtype=like.dtype, device=like.device)[:, :cols]
+
+
+def norm_residual(h, w_pre=None, o=None, w_post=None, gate=None, rows_per_group=None, alpha=1.0, eps=1e-6,
+                  quantize=False, out=None, stream=None):
+    """The norms after and before a block with its gate and the residual update
+    (fp4_norm_residual) on 2-D CUDA tensors: h' = h + alpha * gate * (o, or its
+    RMS norm times w_post), y = the RMS norm of h' times w_pre.  Returns {"h":
+    h' (h itself without o), "rstd_post", "rstd_pre", and with w_pre "y", or
+    with quantize=True "q", y as an FP8 tensor of 1 x 128 blocks}.  `out` may
+    hold buffers under those names; out["y"] and out["q"] together get both."""
+    _on_current_device(h, "h")
+    _want(h, "h")
+    rows, cols = h.shape
+    out = out or {}
+    if o is None and w_pre is None:
+        raise ValueError("nothing to do: neither o nor w_pre is given")
+    if o is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate belong to a block output o")
+    o, ldo = _mat(o, "o", (rows, cols), h)
+    for w, what in ((w_pre, "w_pre"), (w_post, "w_post")):
+        if w is not None:
+            _want(w, what, shape=(cols,), dtype=h.dtype, like=h)
+    gate, ldg, per = _gate_of(gate, rows_per_group, rows, cols, h)
+    got, h_out, ld_hout = dict(h=h, rstd_post=None, rstd_pre=None), None, 0
+    if o is not None:
+        h_out, ld_hout = _mat(out["h"] if out.get("h") is not None else _blank(h, rows, cols), "out h", (rows, cols), h)
+        got["h"] = h_out
+    if w_post is not None:
+        got["rstd_post"] = _float_vector(out.get("rstd_post"), "rstd_post", (rows,), h)
+    y, ldy, q = None, 0, (None, 0, None)
+    if w_pre is not None:
+        got["rstd_pre"] = _float_vector(out.get("rstd_pre"), "rstd_pre", (rows,), h)
+        if quantize or out.get("q") is not None:
+            got["q"] = out["q"] if out.get("q") is not None else alloc_fp8_block(rows, cols, 1, h.device)
+            q = _fp8_tensor(got["q"], "q", rows, cols, 1, h)
+        if not quantize or out.get("y") is not None:
+            y, ldy = _mat(out["y"] if out.get("y") is not None else _blank(h, rows, cols), "y", (rows, cols), h)
+            got["y"] = y
+    fp4_norm_residual(o, ldo, h, _pitch(h), in_dtype_of(h), rows, cols, w_post, gate, ldg, per, alpha, w_pre, eps,
+                      h_out, ld_hout, y, ldy, *q, got["rstd_post"], got["rstd_pre"], stream)
+    return got
+
+
+def norm_residual_backward(dy, h, rstd_pre=None, w_pre=None, dh_in=None, o=None, w_post=None, rstd_post=None,
+                           gate=None, rows_per_group=None, alpha=1.0, out=None, workspace=None, stream=None):
+    """The gradients of norm_residual (fp4_norm_residual_backward): dy of y, or
+    None without a norm before the block; h the stream that norm_residual
+    returned; dh_in the gradient that reaches it from elsewhere.  Returns
+    {"dh", "do", "dw_pre", "dw_post", "dgate"}, None where it has no meaning;
+    the last three in float32.  `out` may hold buffers under those names."""
+    import torch
+    like = dy if dy is not None else dh_in
+    if like is None:
+        raise ValueError("neither dy nor dh_in is given")
+    _on_current_device(like, "the incoming gradient")
+    rows, cols = like.shape
+    shape = (rows, cols)
+    out = out or {}
+    if (dy is None) != (w_pre is None) or (w_pre is not None and (rstd_pre is None or h is None)):
+        raise ValueError("dy, w_pre, rstd_pre and h go together")
+    if o is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate belong to a block output o")
+    if w_post is not None and rstd_post is None:
+        raise ValueError("w_post and rstd_post go together")
+    dy, lddy = _mat(dy, "dy", shape, like)
+    dh_in, lddhi = _mat(dh_in, "dh_in", shape, like)
+    h, ldh = _mat(h, "h", shape, like) if w_pre is not None else (None, 0)
+    o, ldo = _mat(o, "o", shape, like)
+    for w, what in ((w_pre, "w_pre"), (w_post, "w_post")):
+        if w is not None:
+            _want(w, what, shape=(cols,), dtype=like.dtype, like=like)
+    for r, what, w in ((rstd_pre, "rstd_pre", w_pre), (rstd_post, "rstd_post", w_post)):
+        if w is not None:
+            _float_vector(r, what, (rows,), like)
+    gate, ldg, per = _gate_of(gate, rows_per_group, rows, cols, like)
+    pick = lambda name: out[name] if out.get(name) is not None else _blank(like, rows, cols)  # noqa: E731
+    got = dict(dh=pick("dh"), do=None, dw_pre=None, dw_post=None, dgate=None)
+    dh, lddh = _mat(got["dh"], "out dh", shape, like)
+    d_o, lddo = None, 0
+    if o is not None:
+        d_o, lddo = _mat(pick("do"), "out do", shape, like)
+        got["do"] = d_o
+    if w_pre is not None:
+        got["dw_pre"] = _float_vector(out.get("dw_pre"), "dw_pre", (cols,), like)
+    if w_post is not None:
+        got["dw_post"] = _float_vector(out.get("dw_post"), "dw_post", (cols,), like)
+    if gate is not None:
+        got["dgate"] = _float_vector(out.get("dgate"), "dgate", tuple(gate.shape), like)
+    ws_bytes = fp4_norm_residual_backward_workspace_size(rows, cols, w_pre is not None, w_post is not None,
+                                                         gate is not None, per)
+    if ws_bytes and workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=like.device)
+    fp4_norm_residual_backward(dy, lddy, dh_in, lddhi, h, ldh, o, ldo, in_dtype_of(like), rows, cols, w_post, gate,
+                               ldg, per, alpha, w_pre, rstd_post if w_post is not None else None,
+                               rstd_pre if w_pre is not None else None, dh, lddh, d_o, lddo, got["dw_pre"],
+                               got["dw_post"], got["dgate"], workspace if ws_bytes else None,
+                               workspace.numel() * workspace.element_size() if ws_bytes else 0, stream)
+    return got

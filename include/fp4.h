@@ -458,6 +458,125 @@ fp4_status_t fp4_gemm(fp4_format_t format, int double_block,
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * FP8 with a scale per block of 128.  The linears that a 4-bit recipe keeps in
+ * 8 bits: E4M3 codes with one FP32 scale per block of 128 elements along K,
+ * the block being one line (1 x 128: activations and gradients) or 128 lines
+ * (128 x 128: weights, whose transposed operand then has the same codes).
+ *   codes   uint8 [L, ld]: E4M3 (sign in bit 7), ld >= K, ld % 16 == 0;
+ *           bytes K .. ld - 1 of a line are neither written nor read
+ *   scales  float [ceil(K / 128), n]: n = L rounded up to 128 for 1 x 128
+ *           blocks (the padding is not written), n = ceil(L / 128) for
+ *           128 x 128 blocks; 16-byte aligned
+ * The last block along K, and the last one along the lines, may be partial.
+ */
+
+/* fp4_fp8_block_scales_count -- floats in the scale buffer above (0 for an
+ * empty tensor, or a block_lines other than 1 and 128). */
+size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines);
+
+/*
+ * fp4_fp8_block_quantize -- quantize a [rows, ld] tensor along its rows (lines
+ * are rows, K = cols), its columns (lines are columns, K = rows: the
+ * transposed operand of Dgrad and Wgrad), or both from one read.  With m the
+ * largest |x| of a block:
+ *     s = RN(m / 448)  (1 where that is below the smallest normal binary32),
+ *     r = RN(1 / s),   code = E4M3_rne_satfinite(RN(x r)).
+ *   x, in_dtype, rows, cols, ld   input, as fp4_quantize; any rows and cols
+ *   block_lines     1 or 128
+ *   codes_rows, ld_rows, scales_rows   the rows' result, or codes_rows NULL
+ *   codes_cols, ld_cols, scales_cols   the columns' result, or codes_cols NULL
+ * At least one of the two is wanted.  Errors as fp4_quantize: code and scale
+ * buffers 16-byte aligned, ld_rows and ld_cols multiples of 16.  Outputs may
+ * not overlap the input.  Empty input writes nothing.  Non-finite inputs are
+ * out of scope: their block's codes and scale are unspecified.
+ */
+fp4_status_t fp4_fp8_block_quantize(const void* x, fp4_in_dtype_t in_dtype, int64_t rows, int64_t cols, int64_t ld,
+                                    int block_lines, uint8_t* codes_rows, int64_t ld_rows, float* scales_rows,
+                                    uint8_t* codes_cols, int64_t ld_cols, float* scales_cols, void* stream);
+
+/*
+ * fp4_fp8_block_gemm -- C = A B^T of two such tensors on tcgen05 tensor cores:
+ *     C[i, j] = sum_kc sA[kc, i] sB[kc, j or j / 128] sum_{k in kc} qA[i, k] qB[j, k]
+ * with A [M, K] in 1 x 128 blocks and B [N, K] in b_block_lines x 128 blocks:
+ * 128 for Fprop (Y = X W^T) and Dgrad (dX = dY W, B = W along its columns), 1
+ * for Wgrad (dW = dY^T X, both operands along their columns).  Chunk products
+ * are summed in FP32 by the tensor cores and promoted in FP32 registers.
+ *   lda, ldb  row pitches of the codes in bytes, as above
+ *   c         device, [M, ldc] row-major, fp32 or bf16, ldc >= N
+ * Shape rules: M, N and K may be anything >= 0 (K == 0 gives FP4_ERR_UNSUPPORTED_SHAPE
+ * unless C is empty); code, scale and C pointers 16-byte aligned, ldc * size % 16 == 0.
+ * Columns N .. ldc - 1 of C are left as they were.  The result does not depend
+ * on timing.  A bounded wait that runs out is reported by fp4_last_error().
+ */
+fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float* a_scales, const uint8_t* b_codes,
+                                int64_t ldb, const float* b_scales, int b_block_lines, int64_t M, int64_t N, int64_t K,
+                                void* c, fp4_out_dtype_t out_dtype, int64_t ldc, void* stream);
+
+/*
+ * fp4_norm_residual -- the RMS norms after and before a block, fused with the
+ * block's gate and the residual update, for a stream h and a block output o of
+ * `rows` tokens:
+ *     r  = o rstd_post w_post, rstd_post = 1 / sqrt(mean(o^2) + eps)   (w_post given)
+ *        = o                                                          (w_post NULL)
+ *     h' = h + alpha gate r, rounded to the stream's type             (o NULL: h' = h)
+ *     y  = h' rstd_pre w_pre,  rstd_pre = 1 / sqrt(mean(h'^2) + eps)   (w_pre given)
+ * in binary32 from inputs of type `dtype`.  y is written in that type, as the
+ * E4M3 operand of fp4_fp8_block_gemm (1 x 128 blocks, of the binary32 y), or
+ * both.
+ *   o, ldo          [rows, ldo], or NULL
+ *   h, ldh          [rows, ldh]
+ *   w_post, w_pre   [cols], or NULL
+ *   gate, ld_gate, rows_per_group   [ceil(rows / rows_per_group), ld_gate]:
+ *                   row t uses gate row t / rows_per_group; or NULL (1)
+ *   h_out, ld_hout  [rows, ld_hout]; required with o, unused without; may be h
+ *                   itself (h_out == h and ld_hout == ldh) but overlaps nothing else
+ *   y, ldy          or NULL
+ *   codes, ld_codes, scales   or NULL
+ *   rstd_post, rstd_pre   float [rows], written where the norm is taken
+ * Shape rules: cols <= 16384, any rows; every matrix pointer 16-byte aligned
+ * with a pitch that is a multiple of 16 bytes.  w_pre needs y or codes (and
+ * they need w_pre); w_post and gate need o; eps >= 0 and finite, alpha finite.
+ */
+fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_t ldh, fp4_in_dtype_t dtype,
+                               int64_t rows, int64_t cols, const void* w_post, const void* gate, int64_t ld_gate,
+                               int64_t rows_per_group, float alpha, const void* w_pre, float eps, void* h_out,
+                               int64_t ld_hout, void* y, int64_t ldy, uint8_t* codes, int64_t ld_codes, float* scales,
+                               float* rstd_post, float* rstd_pre, void* stream);
+
+/*
+ * fp4_norm_residual_backward -- the gradients of fp4_norm_residual, given dy
+ * (of y) and dh_in (of h', from what else reads the stream):
+ *     a  = dy w_pre, n2 = h' rstd_pre
+ *     dh = dh_in + rstd_pre (a - n2 mean(a n2)),    dw_pre  = sum_t dy n2
+ *     g' = gate alpha dh, n1 = o rstd_post, b = g' w_post
+ *     do = rstd_post (b - n1 mean(b n1)), or g',    dw_post = sum_t g' n1
+ *     dgate = sum over the group's rows of alpha dh r
+ * dh is the gradient of both h' and h.
+ *   dy, ldy, w_pre, rstd_pre, dw_pre   together, or all NULL (no norm before)
+ *   dh_in, ld_dhin  or NULL (0); at least one of dy and dh_in is needed
+ *   h, ldh          h' as fp4_norm_residual wrote it (needed with w_pre)
+ *   o, ldo, d_o, ld_do   together, or both NULL (no residual update)
+ *   w_post, rstd_post, dw_post   together, or all NULL
+ *   gate, ld_gate, rows_per_group, dgate   together, or NULL
+ *   dh, ld_dh       [rows, ld_dh]; may be dh_in itself
+ *   dw_pre, dw_post   float [cols], overwritten
+ *   dgate           float [ceil(rows / rows_per_group), cols], overwritten
+ *   workspace       fp4_norm_residual_backward_workspace_size() bytes, 16-byte
+ *                   aligned; contents are scratch (partial sums over rows)
+ * Row sums are added in an order fixed by the sizes, so results do not depend
+ * on timing.  Shape rules and errors as fp4_norm_residual.
+ */
+fp4_status_t fp4_norm_residual_backward_workspace_size(int64_t rows, int64_t cols, int has_pre, int has_post,
+                                                       int has_gate, int64_t rows_per_group, size_t* bytes);
+fp4_status_t fp4_norm_residual_backward(const void* dy, int64_t lddy, const void* dh_in, int64_t ld_dhin,
+                                        const void* h, int64_t ldh, const void* o, int64_t ldo, fp4_in_dtype_t dtype,
+                                        int64_t rows, int64_t cols, const void* w_post, const void* gate,
+                                        int64_t ld_gate, int64_t rows_per_group, float alpha, const void* w_pre,
+                                        const float* rstd_post, const float* rstd_pre, void* dh, int64_t ld_dh,
+                                        void* d_o, int64_t ld_do, float* dw_pre, float* dw_post, float* dgate,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fp4_last_error -- synchronizes `stream` and returns (and clears) the device
  * error word the kernels set: FP4_ERR_TIMEOUT when a bounded wait gave up (a
  * GEMM pipeline hand-off, a quantizer ring wait or its grid barrier; the kernel
@@ -487,7 +606,8 @@ void fp4_set_wait_limit(uint32_t polls);
  * 256 x 256 output tiles shared by two SMs through tcgen05 cta_group::2, each
  * SM loading its own A rows and half of B (nonzero, the default), or on single
  * CTAs with 128 x 256 tiles (0).  The products are the same block-scaled dot
- * products either way.  Process-wide; not synchronized with calls in flight on
+ * products either way.  It selects the same for fp4_fp8_block_gemm: 256 x 256
+ * tiles on pairs where they fill the GPU, or 128-line tiles with K split.  Process-wide; not synchronized with calls in flight on
  * other host threads.
  */
 void fp4_set_gemm_cta_pairs(int enable);

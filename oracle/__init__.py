@@ -448,3 +448,109 @@ def gemm_outctl(a: dict, b: dict):
     C4, b4 = gemm(a["fp4"], b["fp4"])
     a8, b8 = fp8_dequantize(a["fp8"]), fp8_dequantize(b["fp8"])
     return C4 + a8 @ b8.T, b4 + np.abs(a8) @ np.abs(b8).T
+
+
+# --------------------------------------------------------------------------- FP8, a scale per block of 128
+
+def fp8_block_quantize(x: np.ndarray, block_lines: int = 1, axis: int = 1) -> dict:
+    """E4M3 with one FP32 scale per block of 128 elements along the lines, of
+    block_lines lines: m = max|x|, s = RN(m / 448) (1 where that is below the
+    smallest normal binary32), r = RN(1 / s), code = E4M3(RN(x r)).  Returns
+    codes [L, K] and scales [L or ceil(L / 128), ceil(K / 128)]."""
+    v = widen(np.ascontiguousarray(x))
+    v = np.ascontiguousarray(v if axis == 1 else v.T)
+    L, K = v.shape
+    nl, nk = -(-L // block_lines), -(-K // 128)
+    scales = np.ones((nl, nk), np.float32)
+    scaled = np.zeros((L, K), np.float32)
+    for k in range(nk):
+        part = v[:, 128 * k:128 * (k + 1)]
+        line_max = np.abs(part).max(axis=1) if L else np.zeros(0, np.float32)
+        for b in range(nl):
+            at = slice(b * block_lines, min(L, (b + 1) * block_lines))
+            s = np.float32(line_max[at].max() / np.float32(448.0))
+            if not s >= np.float32(2.0 ** -126):
+                s = np.float32(1.0)
+            scales[b, k] = s
+            scaled[at, 128 * k:128 * (k + 1)] = part[at] * (np.float32(1.0) / s)
+    codes = np.zeros((L, K), np.uint8)
+    if scaled.size:
+        lib().orc_fp8_encode_array(_ptr(scaled), scaled.size, 1.0, _ptr(codes))
+    return dict(codes=codes, scales=scales, block_lines=block_lines)
+
+
+def fp8_block_dequantize(q: dict) -> np.ndarray:
+    """Exact float64 values code * scale of an FP8 tensor."""
+    L, K = q["codes"].shape
+    s = np.repeat(np.repeat(q["scales"].astype(np.float64), q["block_lines"], 0)[:L], 128, 1)[:, :K]
+    return fp8_dequantize(dict(codes=q["codes"], scale=1.0)) * s
+
+
+def fp8_block_gemm(a: dict, b: dict):
+    """C64 = deq(A) deq(B)^T in float64, and the bound sum_k |a b|."""
+    da, db = fp8_block_dequantize(a), fp8_block_dequantize(b)
+    return da @ db.T, np.abs(da) @ np.abs(db).T
+
+
+# --------------------------------------------------------------------------- norms, gate and residual
+
+def _rms(x: np.ndarray, eps: float) -> np.ndarray:
+    return 1.0 / np.sqrt((x * x).mean(axis=1) + eps)
+
+
+def norm_branch(o, w_post, gate, per, rstd_post):
+    """(r, n1, g) of the residual branch in float64: r = n1 w_post (or o), and
+    the gate spread over the rows (1 without one)."""
+    n1 = o * rstd_post[:, None] if w_post is not None else o
+    r = n1 * w_post if w_post is not None else o
+    g = gate[np.arange(o.shape[0]) // per] if gate is not None else np.ones_like(o)
+    return r, n1, g
+
+
+def norm_residual(h, o=None, w_post=None, gate=None, per=None, alpha=1.0, w_pre=None, eps=1e-6) -> dict:
+    """The forward operator in float64, without roundings: h', y and the two
+    inverse RMS values."""
+    out = dict(rstd_post=None, rstd_pre=None, y=None)
+    if o is not None:
+        if w_post is not None:
+            out["rstd_post"] = _rms(o, eps)
+        r, _, g = norm_branch(o, w_post, gate, per, out["rstd_post"])
+        h = h + alpha * g * r
+    out["h"] = h
+    if w_pre is not None:
+        out["rstd_pre"] = _rms(h, eps)
+        out["y"] = h * out["rstd_pre"][:, None] * w_pre
+    return out
+
+
+def norm_residual_backward(dy, h, rstd_pre, w_pre, dh_in, o, w_post, rstd_post, gate, per, alpha) -> dict:
+    """The gradients in float64 from the formulas.  `size` holds, per result,
+    the sum of the magnitudes that its roundings are relative to."""
+    rows, cols = (dy if dy is not None else dh_in).shape
+    dh = np.zeros((rows, cols)) if dh_in is None else dh_in.copy()
+    size = np.abs(dh)
+    got = dict(dw_pre=None, dw_post=None, dgate=None, do=None, size={})
+    if w_pre is not None:
+        n2, a = h * rstd_pre[:, None], dy * w_pre
+        dh += rstd_pre[:, None] * (a - n2 * (a * n2).mean(axis=1, keepdims=True))
+        size = size + rstd_pre[:, None] * (np.abs(a) + np.abs(n2) * np.abs(a * n2).mean(axis=1, keepdims=True))
+        got["dw_pre"] = (dy * n2).sum(axis=0)
+        got["size"]["dw_pre"] = np.abs(dy * n2).sum(axis=0)
+    got["dh"], got["size"]["dh"] = dh, size
+    if o is None:
+        return got
+    r, n1, g = norm_branch(o, w_post, gate, per, rstd_post)
+    gr, gsize = alpha * g * dh, np.abs(alpha * g) * size
+    if gate is not None:
+        got["dgate"], got["size"]["dgate"] = np.zeros(gate.shape), np.zeros(gate.shape)
+        np.add.at(got["dgate"], np.arange(rows) // per, alpha * dh * r)
+        np.add.at(got["size"]["dgate"], np.arange(rows) // per, np.abs(alpha * r) * size)
+    if w_post is not None:
+        got["dw_post"], got["size"]["dw_post"] = (gr * n1).sum(axis=0), (gsize * np.abs(n1)).sum(axis=0)
+        b, bsize = gr * w_post, gsize * np.abs(w_post)
+        got["do"] = rstd_post[:, None] * (b - n1 * (b * n1).mean(axis=1, keepdims=True))
+        got["size"]["do"] = rstd_post[:, None] * (
+            bsize + np.abs(n1) * (bsize * np.abs(n1)).mean(axis=1, keepdims=True))
+    else:
+        got["do"], got["size"]["do"] = gr, gsize
+    return got

@@ -1,0 +1,187 @@
+"""FP8 with a scale per block of 128 on the GPU against the oracle: codes and
+scales bit for bit, the GEMM within |C - C64| <= 1e-5 sum |a b| (+ half a bf16
+step of the result for bf16 output), on both of its kernels.
+
+The GEMM's bound: a chunk's tensor-core sum of 128 products takes part in at
+most 5 binary32 roundings per K = 32 step and chunk, the scales in 2, and the
+promotion in one per chunk; at K = 14336 (112 chunks) that is under 140
+roundings of 2^-24, 8.4e-6 of sum |a b|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from parity import assert_within_gemm_bound, oracle_input
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fp4(cuda_device):
+    from fp4_block_scaled_h16_b200 import fp4 as m
+    return m
+
+
+def make(rows, cols, seed, dtype=torch.bfloat16, pad=0):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((rows, (cols + 7) // 8 * 8 + pad)).astype(np.float32)
+    x[:, rng.integers(0, cols, max(1, cols // 100))] *= 50.0
+    x[rng.integers(0, rows)] = 0.0                       # a block of zeros
+    x[rng.integers(0, rows)] *= np.float32(2.0 ** -130)  # subnormal quotients
+    return torch.from_numpy(x).to(dtype)[:, :cols]
+
+
+def assert_same(fp4, q, o, what=""):
+    codes, scales = q["codes"].cpu().numpy()[:, :q["K"]], q["scales"].cpu().numpy()
+    n = o["scales"].shape[0]
+    assert (scales[:, :n].T.view(np.uint32) == o["scales"].view(np.uint32)).all(), what + " scales"
+    bad = np.argwhere(codes != o["codes"])
+    assert len(bad) == 0, "%s: %d codes differ, first %s" % (what, len(bad), bad[:3].tolist())
+
+
+SHAPES = [(1, 1), (1, 4096), (3, 130), (128, 128), (127, 129), (129, 127), (300, 513), (1000, 272), (257, 2000)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lines", [1, 128])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("pad", [0, 24])
+def test_quantize_matches_oracle(fp4, dtype, lines, shape, pad):
+    x = make(*shape, seed=shape[0] + shape[1], dtype=dtype, pad=pad)
+    xd = torch.zeros((shape[0], x.stride(0) if shape[0] > 1 else shape[1] + (-shape[1]) % 8 + pad), dtype=dtype).cuda()
+    xd[:, :shape[1]] = x.cuda()
+    if xd.shape[1] > shape[1]:
+        xd[:, shape[1]:] = 1e30                          # never read into a block
+    xd = xd[:, :shape[1]]
+    want = [oracle.fp8_block_quantize(oracle_input(x.contiguous()), lines, axis) for axis in (1, 0)]
+    assert_same(fp4, fp4.fp8_block_quantize(xd, 1, lines), want[0], "rows")
+    assert_same(fp4, fp4.fp8_block_quantize(xd, 0, lines), want[1], "columns")
+    qr, qc = fp4.fp8_block_quantize_both_axes(xd, lines)
+    assert_same(fp4, qr, want[0], "rows of both")
+    assert_same(fp4, qc, want[1], "columns of both")
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+
+
+def test_quantize_writes_nothing_past_its_lines_and_columns(fp4):
+    x = make(130, 200, 5).cuda()
+    qr, qc = fp4.alloc_fp8_block(130, 200), fp4.alloc_fp8_block(200, 130)
+    for q in (qr, qc):
+        q["codes"].fill_(0xA5)
+        q["scales"].fill_(-7.0)
+    fp4.fp8_block_quantize_both_axes(x, out_rows=qr, out_cols=qc)
+    torch.cuda.synchronize()
+    for q in (qr, qc):
+        assert (q["codes"][:, q["K"]:] == 0xA5).all()
+        assert (q["scales"][:, q["lines"]:] == -7.0).all() and (q["scales"][:, :q["lines"]] > 0).all()
+
+
+def test_empty_quantize_and_gemm(fp4):
+    q = fp4.fp8_block_quantize(torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda"))
+    w = fp4.fp8_block_quantize(make(300, 256, 1).cuda(), 1, 128)
+    assert fp4.fp8_block_gemm(q, w).shape == (0, 300)
+
+
+def upload(fp4, o):
+    q = fp4.alloc_fp8_block(o["codes"].shape[0], o["codes"].shape[1], o["block_lines"])
+    q["codes"].fill_(0x7F)                               # NaN codes past K: never read into a sum
+    q["codes"][:, :q["K"]] = torch.from_numpy(o["codes"]).cuda()
+    q["scales"].fill_(float("nan"))                      # lines past the last: never in a stored element
+    q["scales"][:, :o["scales"].shape[0]] = torch.from_numpy(np.ascontiguousarray(o["scales"].T)).cuda()
+    return q
+
+
+def check_gemm(fp4, M, N, K, b_lines, out_bf16, seed, pitch_extra=0):
+    rng = np.random.default_rng(seed)
+    a = rng.standard_normal((M, K)).astype(np.float32) * np.exp(rng.standard_normal((M, 1))).astype(np.float32)
+    b = rng.standard_normal((N, K)).astype(np.float32) * 0.05
+    oa, ob = oracle.fp8_block_quantize(a, 1), oracle.fp8_block_quantize(b, b_lines)
+    ld = (N + 7) // 8 * 8 + pitch_extra
+    buf = torch.full((M + 1, ld), -77.0, dtype=torch.bfloat16 if out_bf16 else torch.float32, device="cuda")
+    fp4.fp8_block_gemm(upload(fp4, oa), upload(fp4, ob), fp4.FP4_OUT_BF16 if out_bf16 else fp4.FP4_OUT_F32,
+                       out=buf[:M, :N])
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+    C64, bound = oracle.fp8_block_gemm(oa, ob)
+    assert_within_gemm_bound(buf[:M, :N].float().cpu().numpy(), C64, bound, out_bf16, "%s" % ((M, N, K, b_lines),))
+    assert (buf[:M, N:] == -77.0).all() and (buf[M] == -77.0).all()
+
+
+SMALL = [(1, 128, 128), (1, 1, 1), (1, 4096, 512), (2, 130, 257), (7, 300, 1000), (16, 256, 4096), (17, 129, 640),
+         (33, 1000, 384), (64, 128, 2048), (65, 513, 130), (130, 100, 129), (200, 1000, 1536)]
+
+
+@pytest.mark.parametrize("out_bf16", [False, True])
+@pytest.mark.parametrize("b_lines", [1, 128])
+@pytest.mark.parametrize("shape", SMALL)
+def test_gemm_small(fp4, shape, b_lines, out_bf16):
+    check_gemm(fp4, *shape, b_lines, out_bf16, seed=sum(shape))
+
+
+# outputs that run on CTA pairs: whole and ragged tiles, one chunk and many,
+# fewer tiles than pairs and several waves
+LARGE = [(1280, 2048, 256), (2300, 1900, 130), (1111, 2999, 1025), (2560, 2560, 100), (4096, 2300, 640)]
+
+
+@pytest.mark.parametrize("out_bf16", [False, True])
+@pytest.mark.parametrize("b_lines", [1, 128])
+@pytest.mark.parametrize("shape", LARGE)
+def test_gemm_large(fp4, shape, b_lines, out_bf16):
+    check_gemm(fp4, *shape, b_lines, out_bf16, seed=sum(shape), pitch_extra=16)
+
+
+@pytest.mark.parametrize("b_lines", [1, 128])
+def test_gemm_large_without_pairs(fp4, b_lines):
+    fp4.fp4_set_gemm_cta_pairs(False)
+    try:
+        check_gemm(fp4, 1111, 2999, 1025, b_lines, True, seed=8)
+    finally:
+        fp4.fp4_set_gemm_cta_pairs(True)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 14336), (1300, 2100, 14336)])
+def test_gemm_long_k(fp4, M, N, K):
+    check_gemm(fp4, M, N, K, 128, False, seed=K)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 640, 8192), (2048, 2304, 2048)])
+def test_gemm_is_deterministic_and_row_independent(fp4, M, N, K):
+    g = torch.Generator().manual_seed(2)
+    x, w = torch.randn((M, K), generator=g).cuda(), torch.randn((N, K), generator=g).cuda()
+    qa, qb = fp4.fp8_block_quantize(x), fp4.fp8_block_quantize(w, 1, 128)
+    first = fp4.fp8_block_gemm(qa, qb)
+    for _ in range(3):
+        assert torch.equal(fp4.fp8_block_gemm(qa, qb), first)
+
+
+@pytest.mark.parametrize("M,N,K,b_lines", [(4, 256, 8192, 128), (4, 256, 8192, 1), (2304, 2304, 8192, 128),
+                                           (2304, 2304, 8192, 1)])
+def test_gemm_wait_timeout_is_reported_and_recoverable(fp4, M, N, K, b_lines):
+    g = torch.Generator().manual_seed(3)
+    qa = fp4.fp8_block_quantize(torch.randn((M, K), generator=g).cuda())
+    qb = fp4.fp8_block_quantize(torch.randn((N, K), generator=g).cuda(), 1, b_lines)
+    before = fp4.fp8_block_gemm(qa, qb)
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+    fp4.fp4_set_wait_limit(1)
+    try:
+        fp4.fp8_block_gemm(qa, qb)
+        status = fp4.fp4_last_error()
+    finally:
+        fp4.fp4_set_wait_limit(0)
+    assert status == fp4.FP4_ERR_TIMEOUT, fp4.fp4_status_string(status)
+    after = fp4.fp8_block_gemm(qa, qb)
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+    assert torch.equal(before, after)
+
+
+def test_two_streams_at_once(fp4):
+    g = torch.Generator().manual_seed(4)
+    x, w = torch.randn((64, 4096), generator=g).cuda(), torch.randn((1024, 4096), generator=g).cuda()
+    qb = fp4.fp8_block_quantize(w, 1, 128)
+    want = fp4.fp8_block_gemm(fp4.fp8_block_quantize(x), qb)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams * 4:
+        qa = fp4.fp8_block_quantize(x, stream=s)
+        outs.append(fp4.fp8_block_gemm(qa, qb, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)

@@ -1,0 +1,219 @@
+"""The norms around a block with gate and residual update, and their gradients,
+on the GPU against the float64 formulas of the oracle.
+
+Tolerances count roundings of u = 2^-24 relative to the sum of the magnitudes
+that enter.  A row sum adds at most 32 products in a thread, 5 steps of a warp
+and 16 warps: 53 roundings, and the mean, eps, square root and reciprocal 4
+more, halved by the square root in an inverse RMS: 31.  With the products after
+it the forward results stay under 40 u.  Backward, a mean of products takes 56
+and the values in it up to 6: 70 u for dh; do adds a second such mean of values
+that are off by 70 u: 140 u.  A column sum adds at most rows / 296 + 1 rows in a
+CTA and 296 / 8 + 8 partial sums, 60 for the sizes here: 80 u for dw_pre, 220 u
+for dw_post and dgate, whose terms hold dh.  A result in bf16 adds half a step,
+2^-8 of it.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def fp4(cuda_device):
+    from fp4_block_scaled_h16_b200 import fp4 as m
+    return m
+
+
+def half_step(dtype):
+    return 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+
+
+def wide(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def matrix(g, rows, cols, dtype, pad=0, scale=1.0):
+    t = torch.full((rows, (cols + 7) // 8 * 8 + pad), 1e30, dtype=dtype, device="cuda")
+    t[:, :cols] = (torch.randn((rows, cols), generator=g) * scale).to(dtype).cuda()
+    return t[:, :cols]
+
+
+def inputs(rows, cols, dtype, post, per, pad, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    vec = lambda: (1 + 0.2 * torch.randn(cols, generator=g)).to(dtype).cuda()  # noqa: E731
+    return dict(h=matrix(g, rows, cols, dtype, pad, scale), o=matrix(g, rows, cols, dtype, pad, scale),
+                w_post=vec() if post else None, w_pre=vec(),
+                gate=matrix(g, (rows + per - 1) // per, cols, dtype, pad) if per else None)
+
+
+def assert_close(got, want, tol, what):
+    got = wide(got)
+    assert got.shape == want.shape, what
+    bad = np.argwhere(~(np.abs(got - want) <= tol))
+    assert len(bad) == 0, "%s: %d of %d off, first %s got %r want %r tol %r" % (
+        what, len(bad), got.size, bad[0].tolist(), got[tuple(bad[0])], want[tuple(bad[0])],
+        np.broadcast_to(tol, want.shape)[tuple(bad[0])])
+
+
+CASES = [(1, 1), (1, 8), (1, 4096), (5, 7), (3, 2048), (130, 1003), (300, 128), (17, 2056), (9, 5120), (6, 8200),
+         (700, 264), (3, 16384), (2, 16377)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", CASES)
+@pytest.mark.parametrize("post,per", [(True, 0), (True, 3), (False, 0), (False, 1), (True, 1000)])
+def test_forward_and_backward(fp4, dtype, shape, post, per):
+    rows, cols = shape
+    alpha, eps = 0.75, 1e-5
+    t = inputs(rows, cols, dtype, post, per, pad=16, seed=rows + cols)
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"], gate=t["gate"],
+                          rows_per_group=per or None, alpha=alpha, eps=eps)
+    w = {k: wide(v) for k, v in t.items()}
+    ref = oracle.norm_residual(w["h"], w["o"], w["w_post"], w["gate"], per, alpha, None, eps)
+    size = np.abs(w["h"]) + np.abs(ref["h"] - w["h"])
+    half = half_step(dtype)
+    assert_close(f["h"], ref["h"], 40 * U * size + half * np.abs(ref["h"]) * (1 + 40 * U), "h'")
+    if post:
+        assert_close(f["rstd_post"], ref["rstd_post"], 32 * U * ref["rstd_post"], "rstd_post")
+    kept = wide(f["h"])                                  # the norm takes the stored stream
+    ref2 = oracle.norm_residual(kept, w_pre=w["w_pre"], eps=eps)
+    assert_close(f["rstd_pre"], ref2["rstd_pre"], 32 * U * ref2["rstd_pre"], "rstd_pre")
+    assert_close(f["y"], ref2["y"], (40 * U + half) * np.abs(ref2["y"]), "y")
+
+    g = torch.Generator().manual_seed(cols)
+    dy, dh_in = (matrix(g, rows, cols, dtype, 16) for _ in range(2))
+    b = fp4.norm_residual_backward(dy, f["h"], f["rstd_pre"], w_pre=t["w_pre"], dh_in=dh_in, o=t["o"],
+                                   w_post=t["w_post"], rstd_post=f["rstd_post"], gate=t["gate"],
+                                   rows_per_group=per or None, alpha=alpha)
+    r = oracle.norm_residual_backward(wide(dy), kept, wide(f["rstd_pre"]), w["w_pre"], wide(dh_in), w["o"],
+                                      w["w_post"], wide(f["rstd_post"]), w["gate"], per, alpha)
+    for name, count in (("dh", 70), ("do", 140), ("dw_pre", 80), ("dw_post", 220), ("dgate", 220)):
+        if r[name] is None:
+            assert b[name] is None
+            continue
+        tol = count * U * r["size"][name] + (half * np.abs(r[name]) if name in ("dh", "do") else 0.0)
+        assert_close(b[name], r[name], tol, name)
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(4, 640), (2, 1000)])
+def test_parts_of_the_operator(fp4, dtype, shape):
+    """Each half alone: a norm without an update, an update without a norm, and their gradients."""
+    rows, cols = shape
+    t = inputs(rows, cols, dtype, True, 0, 0, 3)
+    w = {k: wide(v) for k, v in t.items()}
+    half = half_step(dtype)
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"])
+    assert f["h"] is t["h"] and f["rstd_post"] is None
+    ref = oracle.norm_residual(w["h"], w_pre=w["w_pre"])
+    assert_close(f["y"], ref["y"], (40 * U + half) * np.abs(ref["y"]), "y")
+    f2 = fp4.norm_residual(t["h"], o=t["o"], alpha=-2.0)
+    ref2 = oracle.norm_residual(w["h"], w["o"], alpha=-2.0)
+    assert "y" not in f2 and f2["rstd_pre"] is None
+    assert_close(f2["h"], ref2["h"], 2 * U * (np.abs(w["h"]) + 2 * np.abs(w["o"])) + half * np.abs(ref2["h"]), "h'")
+    b = fp4.norm_residual_backward(t["o"], t["h"], f["rstd_pre"], w_pre=t["w_pre"])
+    r = oracle.norm_residual_backward(w["o"], w["h"], wide(f["rstd_pre"]), w["w_pre"], None, None, None, None, None, 0, 1)
+    assert b["do"] is None and b["dgate"] is None
+    assert_close(b["dh"], r["dh"], 70 * U * r["size"]["dh"] + half * np.abs(r["dh"]), "dh")
+    assert_close(b["dw_pre"], r["dw_pre"], 80 * U * r["size"]["dw_pre"], "dw_pre")
+    b = fp4.norm_residual_backward(None, None, dh_in=t["h"], o=t["o"], alpha=-2.0)
+    assert torch.equal(b["dh"], t["h"]) and torch.equal(b["do"], (-2.0 * t["h"].float()).to(dtype))
+
+
+def test_norm_into_the_fp8_operand(fp4):
+    """Codes of the binary32 y: within one E4M3 step, and exact off the borders; y and codes may be asked for together."""
+    rows, cols = 37, 1000
+    t = inputs(rows, cols, torch.bfloat16, True, 5, 0, 9)
+    out = dict(y=torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda"))
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"], gate=t["gate"], rows_per_group=5,
+                          quantize=True, out=out)
+    y = oracle.norm_residual(wide(f["h"]), w_pre=wide(t["w_pre"]))["y"]
+    assert_close(f["y"], y, (40 * U + 2.0 ** -8) * np.abs(y), "y")
+    o = oracle.fp8_block_quantize(y.astype(np.float32))
+    s = f["q"]["scales"].cpu().numpy()[:, :rows].T
+    assert (np.abs(s - o["scales"]) <= 42 * U * o["scales"]).all()
+    codes = f["q"]["codes"].cpu().numpy()[:, :cols]
+    # y is off by 40 u, its scale by 42 u, the reciprocal and the product by one
+    # each, so a code may differ only by one step and only where the exact
+    # quotient lies within 84 u of the middle between the two codes (ties are
+    # common: rstd cancels in y / max y, and bf16 factors make short quotients)
+    differ = codes != o["codes"]
+    value = lambda c: oracle.fp8_dequantize(dict(codes=c.reshape(1, -1), scale=1.0))[0]  # noqa: E731
+    got, want = codes[differ], o["codes"][differ]
+    assert (np.abs(got.astype(int) - want.astype(int)) <= 1).all()
+    top = np.stack([np.abs(y[:, k:k + 128]).max(axis=1) for k in range(0, cols, 128)], axis=1)
+    quotient = (y / (np.repeat(top, 128, axis=1)[:, :cols] / 448))[differ]
+    middle = (value(got) + value(want)) / 2
+    assert (np.abs(quotient - middle) <= 84 * U * np.abs(quotient)).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 256), (1, 130)])
+def test_zero_rows_and_eps_zero(fp4, rows, cols):
+    h = torch.zeros((rows, (cols + 7) // 8 * 8), device="cuda")[:, :cols]
+    w = torch.ones(cols, device="cuda")
+    f = fp4.norm_residual(h, w_pre=w, eps=1e-6, quantize=True)
+    assert (f["q"]["codes"][:, :cols] == 0).all() and (f["q"]["scales"][:, :rows] == 1).all()
+    f = fp4.norm_residual(torch.ones_like(h), w_pre=w, eps=0.0)
+    assert torch.equal(f["y"], torch.ones_like(h))
+
+
+def test_in_place_stream_and_gradient(fp4):
+    t = inputs(50, 520, torch.bfloat16, True, 0, 0, 12)
+    kw = dict(w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"])
+    want = fp4.norm_residual(t["h"], **kw)
+    h = t["h"].clone()
+    got = fp4.norm_residual(h, out=dict(h=h), **kw)
+    assert got["h"] is h and torch.equal(h, want["h"]) and torch.equal(got["y"], want["y"])
+    dy, dh_in = torch.randn_like(t["h"]), torch.randn_like(t["h"])
+    bw = dict(w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"], rstd_post=want["rstd_post"])
+    ref = fp4.norm_residual_backward(dy, want["h"], want["rstd_pre"], dh_in=dh_in, **bw)
+    got = fp4.norm_residual_backward(dy, want["h"], want["rstd_pre"], dh_in=dh_in, out=dict(dh=dh_in), **bw)
+    for k in ("dh", "do", "dw_pre", "dw_post"):
+        assert torch.equal(got[k], ref[k]), k
+
+
+def test_nothing_is_written_past_rows_and_columns(fp4):
+    rows, cols = 11, 130
+    t = inputs(rows, cols, torch.bfloat16, True, 4, 0, 13)
+    room = lambda dt: torch.full((rows + 2, cols + 22), 5.0, dtype=dt, device="cuda")  # noqa: E731
+    bufs = {k: room(torch.bfloat16) for k in ("h", "y", "dh", "do")}
+    view = {k: b[1:rows + 1, :cols] for k, b in bufs.items()}
+    # rows 1.. of a pitch of 152 elements start 304 bytes in: 16-byte aligned
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"], gate=t["gate"], rows_per_group=4,
+                          out=dict(h=view["h"], y=view["y"]))
+    flat = torch.full((3 * cols + 10,), 5.0, device="cuda")
+    fp4.norm_residual_backward(t["h"], f["h"], f["rstd_pre"], w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"],
+                               rstd_post=f["rstd_post"], gate=t["gate"], rows_per_group=4,
+                               out=dict(dh=view["dh"], do=view["do"], dgate=flat[:3 * cols].view(3, cols)))
+    torch.cuda.synchronize()
+    for k, b in bufs.items():
+        assert (b[0] == 5).all() and (b[-1] == 5).all() and (b[:, cols:] == 5).all(), k
+    assert (flat[3 * cols:] == 5).all()
+
+
+def test_empty_batch(fp4):
+    h = torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    f = fp4.norm_residual(h, w_pre=w, o=h, w_post=w)
+    assert f["y"].shape == (0, 256)
+    dw = torch.full((256,), 3.0, device="cuda")
+    b = fp4.norm_residual_backward(h, h, f["rstd_pre"], w_pre=w, o=h, w_post=w, rstd_post=f["rstd_post"],
+                                   out=dict(dw_pre=dw))
+    assert (dw == 0).all() and (b["dw_post"] == 0).all()
+
+
+def test_gradients_do_not_depend_on_timing(fp4):
+    t = inputs(4000, 1000, torch.bfloat16, True, 700, 0, 15)
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"], gate=t["gate"], rows_per_group=700)
+    run = lambda: fp4.norm_residual_backward(t["o"], f["h"], f["rstd_pre"], w_pre=t["w_pre"], o=t["o"],  # noqa: E731
+                                             w_post=t["w_post"], rstd_post=f["rstd_post"], gate=t["gate"],
+                                             rows_per_group=700)
+    first = run()
+    for _ in range(3):
+        again = run()
+        assert all(torch.equal(first[k], again[k]) for k in first)
