@@ -41,9 +41,13 @@ namespace {
 
 constexpr int PM = 256, PN = 256;        // tile of a CTA pair
 constexpr int BK = 128;                  // K elements (bytes) per stage: one scale chunk
-constexpr int NUM_THREADS = 384;
-constexpr int PROMO_WARPS = 8;
-constexpr int STAGES = 5;
+constexpr int PROMO_WARPS = 16;
+constexpr int NUM_THREADS = 128 + 32 * PROMO_WARPS;
+constexpr int COLS = PN / (PROMO_WARPS / 4);         // columns of the tile per promotion warp
+// registers per thread: at launch, of warps 0-3, and of the promotion warps
+constexpr int REGS_LAUNCH = 96, REGS_LEAD = 32, REGS_PROMO = 112;
+static_assert(128 * REGS_LEAD + 32 * PROMO_WARPS * REGS_PROMO <= NUM_THREADS * REGS_LAUNCH, "register split");
+constexpr int STAGES = 4;
 constexpr int SC_SLOTS = 8;              // ring of scale slots
 constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
@@ -56,9 +60,8 @@ constexpr unsigned int ERR_TIMEOUT = 7u;
 static_assert(SMEM <= 232448u, "shared memory");
 
 struct PairParams {
-    const float* sa;          // [chunks, lpa]
-    const float* sb;          // [chunks, lpb]
-    int64_t lpa, lpb;
+    const float* sb;          // [chunks, lpb] (128 x 128 blocks)
+    int64_t lpb;
     void* c;
     int64_t ldc;
     int M, N, chunks;
@@ -87,7 +90,10 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, 
 template <bool VEC, bool OUT_BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                      const __grid_constant__ CUtensorMap tmC, const PairParams p) {
+    // bytes of one fill of a stage and its scale slot, per CTA
+    constexpr uint32_t FILL_BYTES = STAGE_BYTES + 512u + (VEC ? PN * 4u : 0u);
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned base, at the same offset in both CTAs
     const uint32_t raw = sm100::smem_u32(smem_raw);
@@ -96,9 +102,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     uint8_t* sc_ring = epi_bufs + PROMO_WARPS * EPI_BUF;
     uint64_t* full = reinterpret_cast<uint64_t*>(sc_ring + SC_SLOTS * SC_BYTES);
     uint64_t* empty = full + STAGES;
-    uint64_t* sfull = empty + STAGES;
-    uint64_t* sempty = sfull + SC_SLOTS;
-    uint64_t* pfull = sempty + SC_SLOTS;
+    uint64_t* pfull = empty + STAGES;
     uint64_t* pempty = pfull + 2;
     uint64_t* drain = pempty + 2;
     uint64_t* peer_done = drain + 1;
@@ -115,10 +119,6 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         for (int s = 0; s < STAGES; ++s) {
             sm100::mbar_init(&full[s], 1);
             sm100::mbar_init(&empty[s], 1);
-        }
-        for (int s = 0; s < SC_SLOTS; ++s) {
-            sm100::mbar_init(&sfull[s], 1);
-            sm100::mbar_init(&sempty[s], PROMO_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
             sm100::mbar_init(&pfull[b], 1);
@@ -143,14 +143,13 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
-        // 384 threads x 168 registers at launch = 128 x 40 + 256 x 232
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LEAD));
         if (warp == 0) {
             // -------------------------------------------------------- producer
             if (sm100::elect_one()) {
                 int stage = 0, slot = 0;
-                uint32_t phase = 0, sphase = 0;
-                uint32_t fills = 0, sfills = 0;
+                uint32_t phase = 0;
+                uint32_t fills = 0;
                 bool ok = true;
                 for (int u = pair; u < tiles && ok; u += pairs) {
                     int tm_, tn_;
@@ -158,34 +157,25 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     const int n0 = tn_ * PN;
                     const int ma = tm_ * PM + 128 * (int)rank;       // this CTA's rows of A
                     const int nb = n0 + 128 * (int)rank;             // ... and lines of B
-                    // scale bytes that exist: scale rows are padded to 128 lines
-                    const uint32_t sa_bytes = ma < p.lpa ? 512u : 0u;
-                    const uint32_t sb_bytes = !VEC ? 0u : (n0 + 128 < p.lpb ? 1024u : 512u);
                     for (int kc = 0; kc < p.chunks; ++kc) {
-                        if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, p.wait_limit, abort_flag) ||
-                            !sm100::mbar_wait(&sempty[slot], sphase ^ 1u, p.wait_limit, abort_flag)) {
+                        if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, p.wait_limit, abort_flag)) {
                             raise_timeout(p, abort_flag);
                             ok = false;
                             break;
                         }
                         uint8_t* st = smem + stage * STAGE_BYTES;
+                        uint8_t* sc = sc_ring + slot * SC_BYTES;
                         const uint32_t bar = sm100::cluster_addr(&full[stage], 0);
-                        if (rank == 0) sm100::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
+                        if (rank == 0) sm100::mbar_arrive_expect_tx(&full[stage], 2 * FILL_BYTES);
                         sm100::tma_load_2d_pair(st, &tmA, kc * BK, ma, bar);
                         sm100::tma_load_2d_pair(st + A_BYTES, &tmB, kc * BK, nb, bar);
+                        sm100::tma_load_2d_pair(sc, &tmSA, ma, kc, bar);
+                        if (VEC) sm100::tma_load_2d_pair(sc + 512, &tmSB, n0, kc, bar);
                         ++fills;
-                        uint8_t* sc = sc_ring + slot * SC_BYTES;
-                        sm100::mbar_arrive_expect_tx(&sfull[slot], sa_bytes + sb_bytes);
-                        if (sa_bytes) sm100::bulk_load(sc, p.sa + kc * p.lpa + ma, sa_bytes, &sfull[slot]);
-                        if (VEC) sm100::bulk_load(sc + 512, p.sb + kc * p.lpb + n0, sb_bytes, &sfull[slot]);
-                        ++sfills;
                         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                        if (++slot == SC_SLOTS) { slot = 0; sphase ^= 1u; }
+                        if (++slot == SC_SLOTS) slot = 0;
                     }
                 }
-                for (int s = 0; s < SC_SLOTS; ++s)
-                    if (sfills > (uint32_t)s)
-                        sm100::mbar_wait(&sfull[s], ((sfills - 1u - s) / SC_SLOTS) & 1u, DRAIN_LIMIT, nullptr);
                 if (rank == 1) {
                     // report the fills to the leader, whose barriers count their bytes
                     sm100::st_cluster_u32(sm100::cluster_addr(const_cast<uint32_t*>(peer_fills), 0), fills);
@@ -202,13 +192,13 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         const uint32_t s = i % STAGES;
                         if (i >= (uint32_t)STAGES)
                             sm100::mbar_wait(&full[s], ((i - STAGES) / STAGES) & 1u, DRAIN_LIMIT, nullptr);
-                        sm100::mbar_arrive_expect_tx(&full[s], STAGE_BYTES);
+                        sm100::mbar_arrive_expect_tx(&full[s], FILL_BYTES);
                     }
                     for (uint32_t i = pf; i < lf; ++i) {          // this CTA's half only: the peer's never comes
                         const uint32_t s = i % STAGES;
                         if (i >= (uint32_t)STAGES)
                             sm100::mbar_wait(&full[s], ((i - STAGES) / STAGES) & 1u, DRAIN_LIMIT, nullptr);
-                        sm100::mbar_complete_tx(&full[s], STAGE_BYTES);
+                        sm100::mbar_complete_tx(&full[s], FILL_BYTES);
                     }
                     const uint32_t last = lf > pf ? lf : pf;
                     for (int s = 0; s < STAGES; ++s)
@@ -254,56 +244,51 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_PROMO));
         // ------------------------------------------------------------ promotion and output
-        constexpr int COLS = PN / 2;                    // columns per warp
         constexpr int BOX_COLS = OUT_BF16 ? 64 : 32;    // 128 bytes of a row of C
         const int q = warp & 3;                         // TMEM lane quarter of this warp
-        const int half = (warp - 4) >> 2;               // which half of the tile's columns
+        const int cg = (warp - 4) >> 2;                 // which COLS columns of the tile
         uint8_t* buf = epi_bufs + (warp - 4) * EPI_BUF;
         const uint32_t buf_s = sm100::smem_u32(buf);
         const uint32_t leader_pempty = sm100::cluster_addr(pempty, 0);
         int slot = 0, pb = 0;
-        uint32_t sphase = 0, pphase = 0;
+        uint32_t pphase = 0;
         bool ok = true;
         for (int u = pair; u < tiles && ok; u += pairs) {
             int tm_, tn_;
             tile_coords(u, p.tiles_m, p.tiles_n, tm_, tn_);
-            const int n0 = tn_ * PN + half * COLS;
+            const int n0 = tn_ * PN + cg * COLS;
             const int row0 = tm_ * PM + 128 * (int)rank + 32 * q;
             // block scales of B: one value per chunk for this warp's 128 columns
             // (columns past N take the last block's; they are not stored)
             const int nblk = VEC ? 0 : min(n0 / 128, (int)p.lpb - 1);
-            float sb_next = VEC ? 0.0f : __ldg(p.sb + nblk);
+            float sb32 = 0.0f;       // lane l: the scale of chunk 32 (kc / 32) + l
             float2 acc[COLS / 2];
 #pragma unroll
             for (int c = 0; c < COLS / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
             for (int kc = 0; kc < p.chunks; ++kc) {
-                const float sb = sb_next;
-                if (!VEC && kc + 1 < p.chunks) sb_next = __ldg(p.sb + (kc + 1) * p.lpb + nblk);
-                const bool got = sm100::mbar_wait(&sfull[slot], sphase, p.wait_limit, abort_flag) &&
-                                 sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
+                if (!VEC && (kc & 31) == 0) sb32 = __ldg(p.sb + min(kc + lane, p.chunks - 1) * p.lpb + nblk);
+                const float sb = VEC ? 1.0f : __shfl_sync(0xffffffffu, sb32, kc & 31);
+                if (!__all_sync(0xffffffffu, sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag))) {
                     if (lane == 0) raise_timeout(p, abort_flag);
                     ok = false;
                     break;
                 }
                 sm100::tc_fence_after();
+                const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + PN * pb + cg * COLS;
+                // the chunk's scales landed before its MMAs ran
                 const float* sc = reinterpret_cast<const float*>(sc_ring + slot * SC_BYTES);
                 const float sa = sc[32 * q + lane];
                 const float s = VEC ? sa : __fmul_rn(sa, sb);
                 const float2 s2 = make_float2(s, s);
-                const float4* sbv = reinterpret_cast<const float4*>(sc + 128 + half * COLS);
-                const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + PN * pb + half * COLS;
-                // four slices of 32 columns: the next one's TMEM load is in
-                // flight while one is promoted
-                uint32_t r[2][32];
-                sm100::tmem_ld32(base, r[0]);
+                const float4* sbv = reinterpret_cast<const float4*>(sc + 128 + cg * COLS);
 #pragma unroll
                 for (int g = 0; g < COLS / 32; ++g) {
-                    sm100::tmem_ld_wait_on(r[g & 1]);
-                    if (g + 1 < COLS / 32) sm100::tmem_ld32(base + 32 * (g + 1), r[(g + 1) & 1]);
-                    else {
+                    uint32_t r[32];
+                    sm100::tmem_ld32(base + 32 * g, r);
+                    sm100::tmem_ld_wait_on(r);
+                    if (g == COLS / 32 - 1) {
                         sm100::tc_fence_before();
                         __syncwarp();
                         // the tensor core may refill this partial
@@ -311,8 +296,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     }
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        float2 p0 = make_float2(__uint_as_float(r[g & 1][4 * c]), __uint_as_float(r[g & 1][4 * c + 1]));
-                        float2 p1 = make_float2(__uint_as_float(r[g & 1][4 * c + 2]), __uint_as_float(r[g & 1][4 * c + 3]));
+                        float2 p0 = make_float2(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]));
+                        float2 p1 = make_float2(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
                         if (VEC) {
                             const float4 w = sbv[8 * g + c];
                             p0 = __fmul2_rn(p0, make_float2(w.x, w.y));
@@ -322,9 +307,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         acc[16 * g + 2 * c + 1] = __ffma2_rn(p1, s2, acc[16 * g + 2 * c + 1]);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) sm100::mbar_arrive(&sempty[slot]);
-                if (++slot == SC_SLOTS) { slot = 0; sphase ^= 1u; }
+                if (++slot == SC_SLOTS) slot = 0;
                 pb ^= 1;
                 if (pb == 0) pphase ^= 1u;
             }
@@ -390,6 +373,19 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     }
 }
 
+// 2-D map over 1 x 128 scales [chunks, lines]: boxes of `box` lines of one chunk, zeros past the last line
+bool make_scale_map(CUtensorMap* m, const float* scales, int64_t chunks, int64_t lines, int box) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)lines, (cuuint64_t)chunks};
+    cuuint64_t strides[1] = {(cuuint64_t)(lines * 4)};
+    cuuint32_t boxes[2] = {(cuuint32_t)box, 1u};
+    cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), dims, strides, boxes, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool VEC, bool OUT_BF16>
 cudaError_t run_pair(const Fp8GemmArgs& g, cudaStream_t s) {
     static PerDeviceOnce setup;
@@ -410,28 +406,29 @@ cudaError_t run_pair(const Fp8GemmArgs& g, cudaStream_t s) {
         return n > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
     }, &dev);
     if (attr_err != cudaSuccess) return attr_err;
-    CUtensorMap ta, tb, tc;
+    CUtensorMap ta, tb, tsa, tsb, tc;
+    const int64_t chunks = (g.K + BK - 1) / BK;
     if (!make_fp8_map(&ta, g.a_codes, g.M, g.K, g.lda, 128) || !make_fp8_map(&tb, g.b_codes, g.N, g.K, g.ldb, 128) ||
+        !make_scale_map(&tsa, g.a_scales, chunks, fp8_scale_lines(g.M, 1), 128) ||
+        !make_scale_map(&tsb, VEC ? g.b_scales : g.a_scales, chunks, fp8_scale_lines(VEC ? g.N : g.M, 1), PN) ||
         !make_c_map(&tc, g.c, OUT_BF16, g.M, g.N, g.ldc))
         return cudaErrorInvalidValue;
     PairParams p{};
-    p.sa = g.a_scales;
     p.sb = g.b_scales;
-    p.lpa = fp8_scale_lines(g.M, 1);
     p.lpb = fp8_scale_lines(g.N, g.b_lines);
     p.M = (int)g.M;
     p.N = (int)g.N;
     p.c = g.c;
     p.ldc = g.ldc;
     p.odd_n = (g.N * (OUT_BF16 ? 2 : 4)) % 16 != 0;
-    p.chunks = (int)((g.K + BK - 1) / BK);
+    p.chunks = (int)chunks;
     p.tiles_m = (int)((g.M + PM - 1) / PM);
     p.tiles_n = (int)((g.N + PN - 1) / PN);
     p.wait_limit = g.wait_limit;
     p.err = device_error_word();
     const int tiles = p.tiles_m * p.tiles_n;
     const int pairs = tiles < max_pairs[dev] ? tiles : max_pairs[dev];
-    gemm_fp8_pair_kernel<VEC, OUT_BF16><<<2 * pairs, NUM_THREADS, SMEM, s>>>(ta, tb, tc, p);
+    gemm_fp8_pair_kernel<VEC, OUT_BF16><<<2 * pairs, NUM_THREADS, SMEM, s>>>(ta, tb, tsa, tsb, tc, p);
     return cudaGetLastError();
 }
 
