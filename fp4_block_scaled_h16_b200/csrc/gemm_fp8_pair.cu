@@ -9,21 +9,33 @@
 // registers: acc += sA (sB P).  The partial of a chunk is 256 x 256 over a CTA
 // pair (tcgen05.mma cta_group::2 kind::f8f6f4, four of K = 32), 128 x 256 per
 // CTA: 256 TMEM columns, so all 512 columns hold two partials and the tensor
-// core fills one while eight warps promote the other.  Per SM a chunk is 512
-// tensor cycles; its promotion is 32768 multiply-adds, 256 cycles of the FP32
-// pipe (512 when B's scales differ per line), and 128 KB of TMEM reads, 256
-// cycles: it hides behind the tensor core with 128 x 128 blocks of B, and is
-// about level with it with 1 x 128 blocks.
+// core fills one while eight warps promote the other.
+//
+// What bounds it: the hand-over of the two partials.  A chunk is 512 tensor
+// cycles (520 measured with the promotion left out); with it, 790, because a
+// partial is busy for its MMAs (512), until the promotion warps see them
+// complete (240), until those have read it (about 500) and until the issuer
+// sees that (200), and only two fit in TMEM.  What was tried against that, per
+// chunk of 256 columns: halves of 128 columns with four partials, 1480 (the
+// N = 128 MMA takes 1.2 times its share, and every hand-over costs the issuer
+// and each warp as much as a whole chunk's), 850 with an issuer per half; tiles
+// of 160 columns with three partials, 800 for each 160; 16 promotion warps of 64
+// columns, 815.  One thread needs about 800 cycles for a chunk's two waits, four
+// MMAs and two commits beside a busy promotion, so two issuers take turns.  With
+// 1 x 128 blocks of B the promotion's product per element more makes it 1040.
+// QKV Fprop 8192 x 6144 x 4096: 193 us, 2140 TFLOP/s (0.64 of twice the bf16
+// burst rate); Wgrad 4096 x 14336 x 8192 in f32: 563 us, 1710 TFLOP/s.
 //
 // Roles (both CTAs, 384 threads, persistent over pair tiles, one CTA per SM):
 //   warp 0   TMA producer: this CTA's 128 rows of A and 128 lines of B per
-//            chunk (counted on the leader's barrier), and, on a ring of its
-//            own, the chunk's scales of its rows (and of the tile's columns);
-//   warp 1   TMEM; in the leader one thread issues both CTAs' MMAs;
-//   warps 4-11  promotion, 32 rows x 128 columns each (128 accumulators and a
-//            32-column slice per thread; setmaxnreg moves the registers of
-//            warps 0-3 here), then the output: 32-row x 128-byte boxes in
-//            swizzled shared memory and TMA stores.
+//            chunk, and the chunk's scales of its rows (and of the tile's
+//            columns) into a longer ring, all counted on the leader's barrier;
+//   warps 1, 2  (warp 1: TMEM) in the leader, one thread each issues the MMAs
+//            of both CTAs for every other chunk;
+//   warps 4-11  promotion, 32 rows x 128 columns each (128 accumulators and 64
+//            columns in flight per thread; setmaxnreg moves registers of warps
+//            0-3 here), then the output: 32-row x 128-byte boxes in swizzled
+//            shared memory and TMA stores.
 // No load uses cluster multicast.  Every wait is bounded; one that runs out
 // sets the device error word to FP4_ERR_TIMEOUT, and before either CTA exits
 // the leader settles every load either CTA issued, as in gemm_pair.cu.
@@ -41,14 +53,19 @@ namespace {
 
 constexpr int PM = 256, PN = 256;        // tile of a CTA pair
 constexpr int BK = 128;                  // K elements (bytes) per stage: one scale chunk
-constexpr int PROMO_WARPS = 16;
+constexpr int MMA_WARPS = 2;
+constexpr int PROMO_WARPS = 8;
 constexpr int NUM_THREADS = 128 + 32 * PROMO_WARPS;
-constexpr int COLS = PN / (PROMO_WARPS / 4);         // columns of the tile per promotion warp
 // registers per thread: at launch, of warps 0-3, and of the promotion warps
-constexpr int REGS_LAUNCH = 96, REGS_LEAD = 32, REGS_PROMO = 112;
+constexpr int REGS_LAUNCH = 168, REGS_LEAD = 64, REGS_PROMO = 216;
 static_assert(128 * REGS_LEAD + 32 * PROMO_WARPS * REGS_PROMO <= NUM_THREADS * REGS_LAUNCH, "register split");
-constexpr int STAGES = 4;
-constexpr int SC_SLOTS = 8;              // ring of scale slots
+constexpr int COLS = PN / (PROMO_WARPS / 4);         // columns of the tile per promotion warp
+constexpr int STAGES = 5;
+// Ring of scale slots, without barriers of its own: a stage is refilled once its
+// MMAs are done; those were issued once the promotion had read the partial two
+// chunks before, and so was past the scales of the chunk before that one.
+constexpr int SC_SLOTS = 8;
+static_assert(SC_SLOTS >= STAGES + 3, "scales are read before their slot is refilled");
 constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr uint32_t SC_BYTES = 128 * 4 + PN * 4;      // scales of 128 rows and of 256 columns
@@ -105,7 +122,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     uint64_t* pfull = empty + STAGES;
     uint64_t* pempty = pfull + 2;
     uint64_t* drain = pempty + 2;
-    uint64_t* peer_done = drain + 1;
+    uint64_t* peer_done = drain + MMA_WARPS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile uint32_t* peer_fills = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
@@ -124,7 +141,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             sm100::mbar_init(&pfull[b], 1);
             sm100::mbar_init(&pempty[b], 2 * PROMO_WARPS);
         }
-        sm100::mbar_init(drain, 1);
+        for (int w = 0; w < MMA_WARPS; ++w) sm100::mbar_init(&drain[w], 1);
         sm100::mbar_init(peer_done, 1);
         *abort_flag = 0;
         *peer_fills = 0;
@@ -207,38 +224,41 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
             }
             __syncwarp();
-        } else if (warp == 1) {
-            // -------------------------------------------------------- MMA issuer (leader)
+        } else if (warp <= MMA_WARPS) {
+            // -------------------------------------------------------- MMA issuers (leader)
             if (rank == 0 && sm100::elect_one()) {
-                int stage = 0, pb = 0;
+                constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+                int stage = 0, pb = 0, turn = 0;
                 uint32_t phase = 0, pphase = 0;
                 bool ok = true, issued = false;
-                constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
                 for (int u = pair; u < tiles && ok; u += pairs) {
                     for (int kc = 0; kc < p.chunks; ++kc) {
-                        if (!sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag) ||
-                            !sm100::mbar_wait(&pempty[pb], pphase ^ 1u, p.wait_limit, abort_flag)) {
-                            raise_timeout(p, abort_flag);
-                            ok = false;
-                            break;
-                        }
-                        sm100::tc_fence_after();
-                        const uint32_t st = sm100::smem_u32(smem + stage * STAGE_BYTES);
+                        if (turn == warp - 1) {
+                            if (!sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag) ||
+                                !sm100::mbar_wait(&pempty[pb], pphase ^ 1u, p.wait_limit, abort_flag)) {
+                                raise_timeout(p, abort_flag);
+                                ok = false;
+                                break;
+                            }
+                            sm100::tc_fence_after();
+                            const uint32_t st = sm100::smem_u32(smem + stage * STAGE_BYTES);
+                            const uint64_t da = sm100::desc_sw128(st), db = sm100::desc_sw128(st + A_BYTES);
+                            // descriptor addresses count 16 bytes: 32 bytes of K per step
 #pragma unroll
-                        for (int kk = 0; kk < BK / 32; ++kk)
-                            mma_f8_pair(tmem + PN * pb, sm100::desc_sw128(st + 32 * kk),
-                                        sm100::desc_sw128(st + A_BYTES + 32 * kk), idesc, kk > 0 ? 1u : 0u);
-                        issued = true;
-                        sm100::tc_commit_pair_both(&empty[stage]);   // both CTAs' stage free
-                        sm100::tc_commit_pair_both(&pfull[pb]);      // both halves of the partial ready
+                            for (int kk = 0; kk < BK / 32; ++kk)
+                                mma_f8_pair(tmem + PN * pb, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                            issued = true;
+                            sm100::tc_commit_pair_both(&pfull[pb]);      // both CTAs' rows of the partial ready
+                            sm100::tc_commit_pair_both(&empty[stage]);   // both CTAs' stage free
+                        }
+                        if (++turn == MMA_WARPS) turn = 0;
                         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                        pb ^= 1;
-                        if (pb == 0) pphase ^= 1u;
+                        if (++pb == 2) { pb = 0; pphase ^= 1u; }
                     }
                 }
                 if (issued) {
-                    sm100::tc_commit_pair_local(drain);
-                    sm100::mbar_wait(drain, 0, DRAIN_LIMIT, nullptr);
+                    sm100::tc_commit_pair_local(&drain[warp - 1]);
+                    sm100::mbar_wait(&drain[warp - 1], 0, DRAIN_LIMIT, nullptr);
                 }
             }
             __syncwarp();
@@ -254,7 +274,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const uint32_t leader_pempty = sm100::cluster_addr(pempty, 0);
         int slot = 0, pb = 0;
         uint32_t pphase = 0;
-        bool ok = true;
+        bool ok = true, seen = false;
         for (int u = pair; u < tiles && ok; u += pairs) {
             int tm_, tn_;
             tile_coords(u, p.tiles_m, p.tiles_n, tm_, tn_);
@@ -270,7 +290,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             for (int kc = 0; kc < p.chunks; ++kc) {
                 if (!VEC && (kc & 31) == 0) sb32 = __ldg(p.sb + min(kc + lane, p.chunks - 1) * p.lpb + nblk);
                 const float sb = VEC ? 1.0f : __shfl_sync(0xffffffffu, sb32, kc & 31);
-                if (!__all_sync(0xffffffffu, sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag))) {
+                if (!__all_sync(0xffffffffu, seen) &&
+                    !__all_sync(0xffffffffu, sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag))) {
                     if (lane == 0) raise_timeout(p, abort_flag);
                     ok = false;
                     break;
@@ -283,33 +304,38 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 const float s = VEC ? sa : __fmul_rn(sa, sb);
                 const float2 s2 = make_float2(s, s);
                 const float4* sbv = reinterpret_cast<const float4*>(sc + 128 + cg * COLS);
+                // 64 columns in flight at a time
 #pragma unroll
-                for (int g = 0; g < COLS / 32; ++g) {
-                    uint32_t r[32];
-                    sm100::tmem_ld32(base + 32 * g, r);
-                    sm100::tmem_ld_wait_on(r);
-                    if (g == COLS / 32 - 1) {
+                for (int g = 0; g < COLS / 64; ++g) {
+                    uint32_t r[2][32];
+                    sm100::tmem_ld32(base + 64 * g, r[0]);
+                    sm100::tmem_ld32(base + 64 * g + 32, r[1]);
+                    sm100::tmem_ld_wait_on(r[0]);
+                    sm100::tmem_ld_wait_on(r[1]);
+                    if (g == COLS / 64 - 1) {
                         sm100::tc_fence_before();
                         __syncwarp();
                         // the tensor core may refill this partial
                         if (lane == 0) sm100::mbar_arrive_cluster_relaxed(leader_pempty + 8u * (uint32_t)pb);
+                        pb ^= 1;
+                        if (pb == 0) pphase ^= 1u;
+                        seen = sm100::mbar_test_wait(&pfull[pb], pphase);    // the next chunk's, ahead of the sums
                     }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float2 p0 = make_float2(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]));
-                        float2 p1 = make_float2(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
+                    for (int c = 0; c < 16; ++c) {
+                        const uint32_t* v = &r[c >> 3][4 * (c & 7)];
+                        float2 p0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                        float2 p1 = make_float2(__uint_as_float(v[2]), __uint_as_float(v[3]));
                         if (VEC) {
-                            const float4 w = sbv[8 * g + c];
+                            const float4 w = sbv[16 * g + c];
                             p0 = __fmul2_rn(p0, make_float2(w.x, w.y));
                             p1 = __fmul2_rn(p1, make_float2(w.z, w.w));
                         }
-                        acc[16 * g + 2 * c] = __ffma2_rn(p0, s2, acc[16 * g + 2 * c]);
-                        acc[16 * g + 2 * c + 1] = __ffma2_rn(p1, s2, acc[16 * g + 2 * c + 1]);
+                        acc[32 * g + 2 * c] = __ffma2_rn(p0, s2, acc[32 * g + 2 * c]);
+                        acc[32 * g + 2 * c + 1] = __ffma2_rn(p1, s2, acc[32 * g + 2 * c + 1]);
                     }
                 }
                 if (++slot == SC_SLOTS) slot = 0;
-                pb ^= 1;
-                if (pb == 0) pphase ^= 1u;
             }
             if (!ok) break;
             // rows row0 .. row0 + 31 (lane = row), columns n0 .. n0 + 127
