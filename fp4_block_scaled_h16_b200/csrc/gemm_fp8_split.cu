@@ -7,17 +7,18 @@
 //
 // With few tokens the call is bound by reading the weight B once.  So the
 // roles are swapped: a tile is 128 lines of B (the M of the MMA, one TMEM lane
-// each) by NT rows of A (its N, 16 to 128), K is split over a cluster of S
-// CTAs, and each CTA streams its share of B through a ring of 16 KB boxes, all
-// of them in flight at once for the usual shares.  Each 128-K chunk is four
-// kind::f8f6f4 MMAs into one of several TMEM buffers; four warps (one per lane
-// quarter) promote it, acc += P (sA sB), in binary32 registers, because an FP32
-// scale per chunk cannot ride in the tensor core's accumulator.  The S partial
-// tiles are then added in rank order through distributed shared memory, so the
-// result does not depend on timing and no workspace or second launch is needed.
+// each) by NT rows of A (its N, 16 to 64), two CTAs per SM.  Beyond 64 rows a
+// tile is 128 rows of A (the lanes) by 256 lines of B.  K is split over a
+// cluster of up to eight CTAs.  Each 128-K chunk is four kind::f8f6f4 MMAs into
+// one of several TMEM buffers; four warps (eight for 256 lines) promote it,
+// acc += P (sA sB), in binary32 registers, because an FP32 scale per chunk
+// cannot ride in the tensor core's accumulator.  The partial tiles of a cluster are added
+// in rank order through distributed shared memory, so the result does not
+// depend on timing and no workspace or second launch is needed.
 //
-// Roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer (and TMEM),
-// warps 2-5 promotion and output.  Every wait is bounded; one that runs out
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM), warps 2-5
+// promotion; for 256 lines of B two issuers, and promotion by warps 4-11 with
+// the registers of warps 0-3 (setmaxnreg).  All warps write the output.  Every wait is bounded; one that runs out
 // sets the device error word to FP4_ERR_TIMEOUT, and the CTA lets its copies
 // and MMAs in flight land and frees TMEM before it leaves.
 #include <cuda.h>
@@ -32,28 +33,37 @@ namespace fp4 {
 
 namespace {
 
-constexpr int LINES = 128;               // lines of B per tile
+constexpr int LANES = 128;               // the tile's side on the TMEM lanes
 constexpr int BK = 128;                  // K elements (bytes) per stage: one scale chunk
-constexpr int NUM_THREADS = 192;
-constexpr int PROMO_WARPS = 4;
+constexpr int MAX_RANKS = 8;             // CTAs of a cluster, which share a tile's K
 constexpr uint32_t DRAIN_LIMIT = 1u << 22;
 constexpr unsigned int ERR_TIMEOUT = 7u;
 
 template <int NT>
 struct SCfg {
-    static constexpr uint32_t B_BYTES = LINES * BK;
-    static constexpr uint32_t A_BYTES = NT * BK;
-    static constexpr uint32_t SA_BYTES = NT * 4;          // scales of the A rows
-    static constexpr uint32_t SB_BYTES = LINES * 4;       // scales of the B lines (1 x 128 blocks)
-    static constexpr uint32_t STAGE_BYTES = (B_BYTES + A_BYTES + SA_BYTES + SB_BYTES + 1023) / 1024 * 1024;
-    static constexpr int FIT = (int)((232448u - 1024u - 512u) / STAGE_BYTES);
-    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-    static constexpr uint32_t RED_BYTES = NT * LINES * 4; // this CTA's partial tile, over the stages
-    static constexpr uint32_t SMEM = STAGES * STAGE_BYTES + 1024 + 512;
-    static constexpr int PBUF = 4;                        // TMEM buffers of NT columns
-    static constexpr uint32_t TMEM_COLS = PBUF * NT < 32 ? 32 : PBUF * NT;
+    static constexpr bool WIDE = NT == 256;
+    static constexpr int MMA_WARPS = WIDE ? 2 : 1;        // issuers, which take the chunks in turn
+    static constexpr int FIRST = WIDE ? 4 : 2;            // first promotion warp
+    static constexpr int PROMO_WARPS = WIDE ? 8 : 4;
+    static constexpr int THREADS = 32 * (FIRST + PROMO_WARPS);
+    static constexpr int WC = NT / (PROMO_WARPS / 4);     // columns of the N side per promotion warp
+    static constexpr int CTAS = WIDE ? 1 : 2;             // per SM
+    static constexpr uint32_t L_BYTES = LANES * BK;
+    static constexpr uint32_t N_BYTES = NT * BK;
+    static constexpr uint32_t SN_BYTES = NT * 4;          // scales of the tile's N side
+    static constexpr uint32_t SL_BYTES = LANES * 4;       // ... and of its lanes
+    static constexpr uint32_t STAGE_BYTES = (L_BYTES + N_BYTES + SN_BYTES + SL_BYTES + 1023) / 1024 * 1024;
+    static constexpr uint32_t EXTRA = 1024 + 512;         // alignment, barriers
+    static constexpr int STAGES = (int)((232448u / CTAS - 1024u - EXTRA) / STAGE_BYTES);
+    // the partial tile, over the stages: rows of C (NT lines of A, or 128), padded
+    // so that eight rows' 16-byte chunks differ in bank
+    static constexpr int RED_PITCH = (WIDE ? NT : LANES) + 4;
+    static constexpr uint32_t RED_BYTES = (WIDE ? LANES : NT) * RED_PITCH * 4;
+    static constexpr uint32_t SMEM = STAGES * STAGE_BYTES + EXTRA;
+    static constexpr int PBUF = WIDE ? 2 : 4;        // TMEM buffers of NT columns
+    static constexpr uint32_t TMEM_COLS = PBUF * NT;
     static_assert(RED_BYTES <= STAGES * STAGE_BYTES, "the partial tile fits over the ring");
-    static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "TMEM allocation");
+    static_assert(TMEM_COLS >= 32 && TMEM_COLS * CTAS <= 512, "TMEM of an SM's CTAs");
 };
 
 struct SplitParams {
@@ -72,24 +82,55 @@ __device__ __forceinline__ void raise_timeout(const SplitParams& p, volatile int
     atomicExch(p.err, ERR_TIMEOUT);
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(caddr) : "memory");
     return v;
 }
 
+// four columns of C from element `at` (a multiple of 4 columns into a row), `n` of them inside C
 template <bool OUT_BF16>
-__device__ __forceinline__ void put(void* c, int64_t at, float v) {
-    if (OUT_BF16) static_cast<__nv_bfloat16*>(c)[at] = __float2bfloat16_rn(v);
-    else static_cast<float*>(c)[at] = v;
+__device__ __forceinline__ void put4(void* c, int64_t at, const float4& v, int n) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    if (OUT_BF16) {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(c) + at;
+        if (n >= 4) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+            *reinterpret_cast<uint2*>(d) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                      *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < n) d[e] = __float2bfloat16_rn(x[e]);
+        }
+    } else {
+        float* d = static_cast<float*>(c) + at;
+        if (n >= 4) {
+            *reinterpret_cast<float4*>(d) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < n) d[e] = x[e];
+        }
+    }
 }
 
-// VEC: B's scales are one per line (1 x 128 blocks), else one per 128 lines
-template <int NT, bool VEC, bool OUT_BF16>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
-gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+// barrier of all threads, reached from different branches
+template <int THREADS>
+__device__ __forceinline__ void all_roles() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// SWAP: lanes are lines of B and the N side rows of A, else the reverse.
+// VEC: B's scales are one per line (1 x 128 blocks), else one per 128 lines.
+template <int NT, bool SWAP, bool VEC, bool OUT_BF16>
+__global__ void __launch_bounds__(SCfg<NT>::THREADS, SCfg<NT>::CTAS)
+gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmN,
                       const SplitParams p) {
     using G = SCfg<NT>;
+    constexpr bool LANE_VEC = !SWAP || VEC;          // a scale per lane
+    constexpr bool N_VEC = SWAP || VEC;              // a scale per column of the N side
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = sm100::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -98,28 +139,28 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     uint64_t* pfull = empty + G::STAGES;
     uint64_t* pempty = pfull + G::PBUF;
     uint64_t* drain = pempty + G::PBUF;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + G::MMA_WARPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;      // the cluster spans the x dimension
-    const int n0 = (int)blockIdx.y * LINES, m0 = (int)blockIdx.z * NT;
+    const int l0 = (int)blockIdx.y * LANES, t0 = (int)blockIdx.z * NT;
     const int kc0 = (int)((int64_t)p.chunks * rank / ranks), kc1 = (int)((int64_t)p.chunks * (rank + 1) / ranks);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::STAGES; ++s) {
             sm100::mbar_init(&full[s], 1);
-            sm100::mbar_init(&empty[s], 1 + PROMO_WARPS);   // the MMAs, and the readers of the scales
+            sm100::mbar_init(&empty[s], 1 + G::PROMO_WARPS);   // the MMAs, and the readers of the scales
         }
         for (int b = 0; b < G::PBUF; ++b) {
             sm100::mbar_init(&pfull[b], 1);
-            sm100::mbar_init(&pempty[b], PROMO_WARPS);
+            sm100::mbar_init(&pempty[b], G::PROMO_WARPS);
         }
-        sm100::mbar_init(drain, 1);
+        for (int w = 0; w < G::MMA_WARPS; ++w) sm100::mbar_init(&drain[w], 1);
         *abort_flag = 0;
         sm100::fence_barrier_init();
-        sm100::prefetch_tmap(&tmA);
-        sm100::prefetch_tmap(&tmB);
+        sm100::prefetch_tmap(&tmL);
+        sm100::prefetch_tmap(&tmN);
     }
     if (warp == 1) {
         sm100::tmem_alloc(tmem_slot, G::TMEM_COLS);
@@ -130,10 +171,21 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     sm100::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    float acc[NT];
+    float* red = reinterpret_cast<float*>(smem);             // the partial tile: [rows of C][columns]
+    const int rows = min(SWAP ? NT : LANES, p.M - (SWAP ? t0 : l0));
+    const int cols = min(SWAP ? LANES : NT, p.N - (SWAP ? l0 : t0));
+    if constexpr (G::WIDE) {         // 384 threads x 168 registers at launch = 128 x 64 + 256 x 216
+        if (warp < G::FIRST) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    }
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (sm100::elect_one()) {
+            const float* sl = SWAP ? p.sb : p.sa;
+            const float* sn = SWAP ? p.sa : p.sb;
+            const int64_t lpl = SWAP ? p.lpb : p.lpa, lpn = SWAP ? p.lpa : p.lpb;
+            // lines past M and N lie in the scale rows' padding to 128
+            const uint32_t sn_bytes = !N_VEC ? 0u : (uint32_t)min((int64_t)NT, lpn - t0) * 4u;
             int stage = 0;
             uint32_t phase = 0, fills = 0;
             for (int kc = kc0; kc < kc1; ++kc) {
@@ -143,13 +195,12 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 }
                 uint8_t* st = smem + stage * G::STAGE_BYTES;
                 sm100::mbar_arrive_expect_tx(&full[stage],
-                                             G::B_BYTES + G::A_BYTES + G::SA_BYTES + (VEC ? G::SB_BYTES : 0u));
-                sm100::tma_load_2d(st, &tmB, kc * BK, n0, &full[stage]);
-                sm100::tma_load_2d(st + G::B_BYTES, &tmA, kc * BK, m0, &full[stage]);
-                // lines past M and N lie in the scale rows' padding to 128
-                sm100::bulk_load(st + G::B_BYTES + G::A_BYTES, p.sa + kc * p.lpa + m0, G::SA_BYTES, &full[stage]);
-                if (VEC)
-                    sm100::bulk_load(st + G::B_BYTES + G::A_BYTES + G::SA_BYTES, p.sb + kc * p.lpb + n0, G::SB_BYTES,
+                                             G::L_BYTES + G::N_BYTES + sn_bytes + (LANE_VEC ? G::SL_BYTES : 0u));
+                sm100::tma_load_2d(st, &tmL, kc * BK, l0, &full[stage]);
+                sm100::tma_load_2d(st + G::L_BYTES, &tmN, kc * BK, t0, &full[stage]);
+                if (N_VEC) sm100::bulk_load(st + G::L_BYTES + G::N_BYTES, sn + kc * lpn + t0, sn_bytes, &full[stage]);
+                if (LANE_VEC)
+                    sm100::bulk_load(st + G::L_BYTES + G::N_BYTES + G::SN_BYTES, sl + kc * lpl + l0, G::SL_BYTES,
                                      &full[stage]);
                 ++fills;
                 if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
@@ -159,49 +210,55 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                     sm100::mbar_wait(&full[s], ((fills - 1u - s) / G::STAGES) & 1u, DRAIN_LIMIT, nullptr);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (sm100::elect_one()) {
-            int stage = 0, pb = 0;
+    } else if (warp < G::FIRST) {
+        // ------------------------------------------------------------ MMA issuers
+        if (warp <= G::MMA_WARPS && sm100::elect_one()) {
+            int stage = 0, pb = 0, turn = 0;
             uint32_t phase = 0, pphase = 0;
             bool issued = false;
             constexpr uint32_t idesc = sm100::idesc_f8_e4m3(NT);
             for (int kc = kc0; kc < kc1; ++kc) {
-                if (!sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag) ||
-                    !sm100::mbar_wait(&pempty[pb], pphase ^ 1u, p.wait_limit, abort_flag)) {
-                    raise_timeout(p, abort_flag);
-                    break;
-                }
-                sm100::tc_fence_after();
-                const uint32_t st = sm100::smem_u32(smem + stage * G::STAGE_BYTES);
+                if (G::MMA_WARPS == 1 || turn == warp - 1) {
+                    if (!sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag) ||
+                        !sm100::mbar_wait(&pempty[pb], pphase ^ 1u, p.wait_limit, abort_flag)) {
+                        raise_timeout(p, abort_flag);
+                        break;
+                    }
+                    sm100::tc_fence_after();
+                    const uint32_t st = sm100::smem_u32(smem + stage * G::STAGE_BYTES);
+                    // descriptor addresses count 16 bytes: 32 bytes of K per step
+                    const uint64_t dl = sm100::desc_sw128(st), dn = sm100::desc_sw128(st + G::L_BYTES);
 #pragma unroll
-                for (int kk = 0; kk < BK / 32; ++kk)
-                    sm100::mma_f8(tmem + NT * pb, sm100::desc_sw128(st + 32 * kk),
-                                  sm100::desc_sw128(st + G::B_BYTES + 32 * kk), idesc, kk > 0 ? 1u : 0u);
-                issued = true;
-                sm100::tc_commit(&empty[stage]);
-                sm100::tc_commit(&pfull[pb]);
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        sm100::mma_f8(tmem + NT * pb, dl + 2 * kk, dn + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                    issued = true;
+                    sm100::tc_commit(&pfull[pb]);
+                    sm100::tc_commit(&empty[stage]);
+                }
+                if (++turn == G::MMA_WARPS) turn = 0;
                 if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
                 if (++pb == G::PBUF) { pb = 0; pphase ^= 1u; }
             }
             if (issued) {
-                sm100::tc_commit(drain);
-                sm100::mbar_wait(drain, 0, DRAIN_LIMIT, nullptr);
+                sm100::tc_commit(&drain[warp - 1]);
+                sm100::mbar_wait(&drain[warp - 1], 0, DRAIN_LIMIT, nullptr);
             }
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ promotion
         const int q = warp & 3;                     // TMEM lane quarter of this warp
+        const int n0 = (warp - G::FIRST) / 4 * G::WC;      // its first column of the N side
+        float2 acc[G::WC / 2];
 #pragma unroll
-        for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
+        for (int c = 0; c < G::WC / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
         int stage = 0, pb = 0;
         uint32_t phase = 0, pphase = 0;
-        const float* sb_block = p.sb + (VEC ? 0 : n0 / 128);
-        float sb_next = (VEC || kc0 >= kc1) ? 0.0f : __ldg(sb_block + kc0 * p.lpb);
+        // columns past N take the last block's scale; they are not stored
+        const float* sb_block = p.sb + (VEC ? 0 : min((int64_t)(SWAP ? l0 : t0 + n0) / 128, p.lpb - 1));
+        float sb32 = 0.0f;                          // lane l: the block scale of chunk kc0 + 32 i + l
         for (int kc = kc0; kc < kc1; ++kc) {
-            float sb = sb_next;
-            if (!VEC && kc + 1 < kc1) sb_next = __ldg(sb_block + (kc + 1) * p.lpb);
+            if (!VEC && ((kc - kc0) & 31) == 0) sb32 = __ldg(sb_block + min(kc + lane, kc1 - 1) * p.lpb);
             const bool ok = sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag) &&
                             sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -209,65 +266,97 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 break;
             }
             sm100::tc_fence_after();
-            const float* sa = reinterpret_cast<const float*>(smem + stage * G::STAGE_BYTES + G::B_BYTES + G::A_BYTES);
-            if (VEC) sb = sa[NT + 32 * q + lane];
-            const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + NT * pb;
+            const float* sn = reinterpret_cast<const float*>(smem + stage * G::STAGE_BYTES + G::L_BYTES + G::N_BYTES);
+            float s = LANE_VEC ? sn[NT + 32 * q + lane] : 1.0f;
+            if (!VEC) s = __fmul_rn(s, __shfl_sync(0xffffffffu, sb32, (kc - kc0) & 31));
+            const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + NT * pb + n0;
+            constexpr int W = G::WC < 32 ? 16 : 32;             // columns per TMEM load
+            constexpr int F = G::WC > W ? 2 : 1;                // loads in flight
 #pragma unroll
-            for (int c0 = 0; c0 < NT; c0 += 16) {
-                uint32_t r[16];
-                sm100::tmem_ld16(base + c0, r);
-                sm100::tmem_ld_wait_on(r);
+            for (int c0 = 0; c0 < G::WC; c0 += F * W) {
+                uint32_t r[F][W];
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    acc[c0 + c] = __fmaf_rn(__uint_as_float(r[c]), __fmul_rn(sa[c0 + c], sb), acc[c0 + c]);
+                for (int f = 0; f < F; ++f) {
+                    if constexpr (W == 16) sm100::tmem_ld16(base + c0 + f * W, r[f]);
+                    else sm100::tmem_ld32(base + c0 + f * W, r[f]);
+                }
+#pragma unroll
+                for (int f = 0; f < F; ++f) sm100::tmem_ld_wait_on(r[f]);
+                if (c0 + F * W == G::WC) {
+                    sm100::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) sm100::mbar_arrive(&pempty[pb]);
+                }
+#pragma unroll
+                for (int c = 0; c < F * W; c += 4) {
+                    float2 w0 = make_float2(s, s), w1 = w0;
+                    if (N_VEC) {
+                        const float4 v = *reinterpret_cast<const float4*>(sn + n0 + c0 + c);
+                        w0 = __fmul2_rn(make_float2(v.x, v.y), w0);
+                        w1 = __fmul2_rn(make_float2(v.z, v.w), w1);
+                    }
+                    const uint32_t* v = &r[c / W][c % W];
+                    float2* d = &acc[(c0 + c) / 2];
+                    d[0] = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), w0, d[0]);
+                    d[1] = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), w1, d[1]);
+                }
             }
-            sm100::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                sm100::mbar_arrive(&pempty[pb]);
-                sm100::mbar_arrive(&empty[stage]);
-            }
+            if (lane == 0) sm100::mbar_arrive(&empty[stage]);
             if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
             if (++pb == G::PBUF) { pb = 0; pphase ^= 1u; }
         }
+        // every load and MMA of this CTA has completed once all roles are here, so
+        // the partial tile may take the ring's place
+        sm100::tc_fence_before();
+        all_roles<G::THREADS>();
+        const int l = 32 * q + lane;
+        if (SWAP) {
+#pragma unroll
+            for (int c = 0; c < G::WC; ++c)
+                if (c < rows) red[c * G::RED_PITCH + l] = (c & 1) ? acc[c / 2].y : acc[c / 2].x;
+        } else if (l < rows) {
+#pragma unroll
+            for (int c = 0; c < G::WC; c += 4)
+                *reinterpret_cast<float4*>(red + l * G::RED_PITCH + n0 + c) =
+                    make_float4(acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
+        }
     }
-
-    // every load and MMA of this CTA has completed once all roles are here, so
-    // the partial tile may take the ring's place
-    sm100::tc_fence_before();
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(smem);             // [NT][128]
-    const int tokens = min(NT, p.M - m0);
-    if (warp >= 2) {
-        const int q = warp & 3;
-        const int line = 32 * q + lane;
-        const int64_t at = (int64_t)m0 * p.ldc + n0 + line;
+    if (warp < G::FIRST) {
+        sm100::tc_fence_before();
+        all_roles<G::THREADS>();
+    }
+    if (ranks > 1) sm100::cluster_sync();
+    else __syncthreads();
+    // the ranks of a cluster share the rows of C; a warp takes 128 columns of a
+    // row at a time, four per thread
+    const int64_t at0 = (int64_t)(SWAP ? t0 : l0) * p.ldc + (SWAP ? l0 : t0);
+    constexpr int SPANS = (SWAP ? LANES : NT) / 128;
+    for (int i = warp; rank + i / SPANS * ranks < rows; i += G::THREADS / 32) {
+        const int row = rank + i / SPANS * ranks, col = i % SPANS * 128 + 4 * lane;
+        if (col >= cols) continue;
+        const float* at = red + row * G::RED_PITCH + col;
+        float4 v;
         if (ranks == 1) {
-            if (n0 + line < p.N) {
-#pragma unroll
-                for (int c = 0; c < NT; ++c)
-                    if (c < tokens) put<OUT_BF16>(p.c, at + c * p.ldc, acc[c]);
-            }
+            v = *reinterpret_cast<const float4*>(at);
         } else {
+            float4 part[8];
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-                if (c < tokens) red[c * LINES + line] = acc[c];
+            for (int r = 0; r < 8; ++r)
+                if (r < ranks) part[r] = ld_cluster_v4(sm100::cluster_addr(at, (uint32_t)r));
+            v = part[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < ranks) {
+                    v.x += part[r].x;
+                    v.y += part[r].y;
+                    v.z += part[r].z;
+                    v.w += part[r].w;
+                }
         }
+        put4<OUT_BF16>(p.c, at0 + (int64_t)row * p.ldc + col, v, cols - col);
     }
-    if (ranks > 1) {
-        sm100::cluster_sync();
-        if (warp >= 2) {
-            const int line = 32 * (warp & 3) + lane;
-            const bool in_n = n0 + line < p.N;
-            for (int c = rank; c < tokens; c += ranks) {
-                float v = 0.0f;
-                for (int r = 0; r < ranks; ++r)
-                    v += ld_cluster_f32(sm100::cluster_addr(red + c * LINES + line, (uint32_t)r));
-                if (in_n) put<OUT_BF16>(p.c, (int64_t)(m0 + c) * p.ldc + n0 + line, v);
-            }
-        }
-        sm100::cluster_sync();                               // no CTA leaves while another reads its tile
-    }
+    if (ranks > 1) sm100::cluster_sync();                    // no CTA leaves while another reads its tile
     if (warp == 1) {
         __syncwarp();
         sm100::tc_fence_after();
@@ -275,17 +364,44 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     }
 }
 
-template <int NT, bool VEC, bool OUT_BF16>
-cudaError_t run_split(const Fp8GemmArgs& g, int ranks, cudaStream_t s) {
+template <int NT, bool SWAP, bool VEC, bool OUT_BF16>
+cudaError_t run_split(const Fp8GemmArgs& g, cudaStream_t s) {
     using G = SCfg<NT>;
     static PerDeviceOnce setup;
-    const cudaError_t attr_err = setup.run([](int) {
-        return cudaFuncSetAttribute(gemm_fp8_split_kernel<NT, VEC, OUT_BF16>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM);
-    });
+    static int max_clusters[kOnceDevices][MAX_RANKS + 1] = {};   // resident at once, one CTA per SM, by cluster size
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(G::THREADS);
+    cfg.dynamicSmemBytes = G::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int dev = 0;
+    const cudaError_t attr_err = setup.run([&](int d) {
+        cudaError_t e = cudaFuncSetAttribute(gemm_fp8_split_kernel<NT, SWAP, VEC, OUT_BF16>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM);
+        for (int r = 1; r <= MAX_RANKS && e == cudaSuccess; ++r) {
+            attr.val.clusterDim.x = (unsigned)r;
+            cfg.gridDim = dim3((unsigned)r * 512);
+            e = cudaOccupancyMaxActiveClusters(&max_clusters[d][r], gemm_fp8_split_kernel<NT, SWAP, VEC, OUT_BF16>, &cfg);
+        }
+        return e;
+    }, &dev);
     if (attr_err != cudaSuccess) return attr_err;
+    const int64_t lanes = SWAP ? g.N : g.M, cols = SWAP ? g.M : g.N;
+    const int64_t tiles = ((lanes + LANES - 1) / LANES) * ((cols + NT - 1) / NT);
+    const int64_t chunks = (g.K + BK - 1) / BK;
+    // K is split as far as all clusters are resident at once, with two chunks per
+    // CTA at least: one token, N = 6144, K = 4096 takes 14.1, 9.5, 8.4, 7.7 and 7.3
+    // us with 1 to 5 ranks, and 11.1 with 6, which do not all fit
+    int ranks = 1;
+    for (int r = 2; r <= MAX_RANKS; ++r)
+        if (tiles <= G::CTAS * max_clusters[dev][r] && chunks >= 2 * r) ranks = r;
     CUtensorMap ta, tb;
-    if (!make_fp8_map(&ta, g.a_codes, g.M, g.K, g.lda, NT) || !make_fp8_map(&tb, g.b_codes, g.N, g.K, g.ldb, LINES))
+    if (!make_fp8_map(&ta, g.a_codes, g.M, g.K, g.lda, SWAP ? NT : LANES) ||
+        !make_fp8_map(&tb, g.b_codes, g.N, g.K, g.ldb, SWAP ? LANES : NT))
         return cudaErrorInvalidValue;
     SplitParams p{};
     p.sa = g.a_scales;
@@ -296,46 +412,28 @@ cudaError_t run_split(const Fp8GemmArgs& g, int ranks, cudaStream_t s) {
     p.ldc = g.ldc;
     p.M = (int)g.M;
     p.N = (int)g.N;
-    p.chunks = (int)((g.K + BK - 1) / BK);
+    p.chunks = (int)chunks;
     p.wait_limit = g.wait_limit;
     p.err = device_error_word();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)((g.N + LINES - 1) / LINES), (unsigned)((g.M + NT - 1) / NT));
-    cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = G::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
+    cfg.gridDim = dim3((unsigned)ranks, (unsigned)((lanes + LANES - 1) / LANES), (unsigned)((cols + NT - 1) / NT));
     attr.val.clusterDim.x = (unsigned)ranks;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_split_kernel<NT, VEC, OUT_BF16>, ta, tb, p);
+    return cudaLaunchKernelEx(&cfg, gemm_fp8_split_kernel<NT, SWAP, VEC, OUT_BF16>, SWAP ? tb : ta, SWAP ? ta : tb, p);
 }
 
-template <int NT>
-cudaError_t run_nt(const Fp8GemmArgs& g, int ranks, cudaStream_t s) {
+template <int NT, bool SWAP>
+cudaError_t run_nt(const Fp8GemmArgs& g, cudaStream_t s) {
     if (g.b_lines == 1)
-        return g.out_bf16 ? run_split<NT, true, true>(g, ranks, s) : run_split<NT, true, false>(g, ranks, s);
-    return g.out_bf16 ? run_split<NT, false, true>(g, ranks, s) : run_split<NT, false, false>(g, ranks, s);
+        return g.out_bf16 ? run_split<NT, SWAP, true, true>(g, s) : run_split<NT, SWAP, true, false>(g, s);
+    return g.out_bf16 ? run_split<NT, SWAP, false, true>(g, s) : run_split<NT, SWAP, false, false>(g, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_fp8_split(const Fp8GemmArgs& g, cudaStream_t s) {
-    const int nt = g.M <= 16 ? 16 : (g.M <= 32 ? 32 : (g.M <= 64 ? 64 : 128));
-    const int64_t tiles = ((g.N + LINES - 1) / LINES) * ((g.M + nt - 1) / nt);
-    const int64_t chunks = (g.K + BK - 1) / BK;
-    // K is split while the tiles alone leave SMs idle, two chunks per CTA at least
-    int ranks = 1;
-    while (ranks < 8 && tiles * ranks * 2 <= num_sms() && chunks >= 4 * ranks) ranks *= 2;
-    switch (nt) {
-    case 16: return run_nt<16>(g, ranks, s);
-    case 32: return run_nt<32>(g, ranks, s);
-    case 64: return run_nt<64>(g, ranks, s);
-    default: return run_nt<128>(g, ranks, s);
-    }
+    if (g.M <= 16) return run_nt<16, true>(g, s);
+    if (g.M <= 32) return run_nt<32, true>(g, s);
+    if (g.M <= 64) return run_nt<64, true>(g, s);
+    return run_nt<256, false>(g, s);
 }
 
 }  // namespace fp4
