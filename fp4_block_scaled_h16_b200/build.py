@@ -16,7 +16,8 @@ SOURCES = ["fp4_api.cu", "quantize.cu", "quantize_rows_f32.cu", "quantize_cols_b
            "requantize_cols.cu", "gemm.cu", "gemm_db.cu", "quantize_noalloc.cu", "rotate.cu", "mxnorm.cu", "ufp4_split.cu",
            "outctl.cu", "gemm_outctl.cu", "gemm_pair.cu", "quantize_dual.cu",
            "fp8_quantize.cu", "gemm_fp8_split.cu", "gemm_fp8_pair.cu", "norm_residual.cu"]
-HEADERS = ["fp4_device.cuh", "internal.h", "sm100.cuh", "quant_common.cuh", "quant_rows.cuh", "quant_cols.cuh"]
+HEADERS = ["fp4_device.cuh", "internal.h", "sm100.cuh", "quant_common.cuh", "quant_rows.cuh", "quant_cols.cuh",
+           "fp8_block.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

@@ -2,14 +2,8 @@
 // along K (fp4_fp8_block_quantize), the operands of the FP8 block-scaled GEMM.
 //
 // A block is 128 consecutive elements of one line (activations, gradients) or
-// of 128 lines (weights).  With m = max |x| over the block:
-//   s = RN(m / 448), 1 where that is below the smallest normal binary32
-//   r = RN(1 / s)
-//   code = E4M3_rne_satfinite(RN(x r))
-// One product per element instead of a division: RN(x r) is within 2^-23 of
-// x / s relative to it (half an ulp from r, half from the product), less than
-// 2^-19 of an E4M3 step.  x r may pass 448 by an ulp; the conversion saturates.
-// s >= 2^-126 keeps r finite.
+// of 128 lines (weights): a scale s = RN(m / 448) from the block's largest
+// magnitude m, and codes E4M3_rne(448 x / m) (fp8_block.cuh).
 //
 // What bounds it: HBM.  Per element 2 B (bf16) or 4 B (f32) are read and 1 B
 // is written per axis.  One CTA of 256 threads takes one 128 x 128 tile: the
@@ -25,6 +19,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "fp8_block.cuh"
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -168,18 +163,7 @@ fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid
             lo = hi = m;
         }
     };
-    auto scale_of = [](float m) {
-        const float s = __fdiv_rn(m, 448.0f);
-        return s >= 1.17549435e-38f ? s : 1.0f;
-    };
-    auto pack4 = [](float a, float b, float c, float d) {
-        uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-        return (uint32_t)lo | ((uint32_t)hi << 16);
-    };
-
-    float tile_s = 1.0f, tile_r = 1.0f;
+    Fp8Block tile;
     if (LINES == 128) {
         load_row();
         float lo, hi;
@@ -190,24 +174,22 @@ fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid
         float mm = part[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) mm = fmaxf(mm, part[i]);
-        tile_s = scale_of(mm);
-        tile_r = __frcp_rn(tile_s);
+        tile = fp8_block(mm);
         if (t == 0) {
-            if (ROWS) p.scales_rows[(int64_t)tc * p.lp_rows + tr] = tile_s;
-            if (COLS) p.scales_cols[(int64_t)tr * p.lp_cols + tc] = tile_s;
+            if (ROWS) p.scales_rows[(int64_t)tc * p.lp_rows + tr] = tile.s;
+            if (COLS) p.scales_cols[(int64_t)tr * p.lp_cols + tc] = tile.s;
         }
     }
     if (ROWS) {
-        float r = tile_r;
+        Fp8Block b = tile;
         if (LINES == 1) {
             load_row();
             float lo, hi;
             max_words(lo, hi);
             float m = fmaxf(lo, hi);
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            const float s = scale_of(m);
-            r = __frcp_rn(s);
-            if (half == 0 && row0 + row < p.rows) p.scales_rows[(int64_t)tc * p.lp_rows + row0 + row] = s;
+            b = fp8_block(m);
+            if (half == 0 && row0 + row < p.rows) p.scales_rows[(int64_t)tc * p.lp_rows + row0 + row] = b.s;
         }
         // 64 codes of the row: four 16-byte chunks (of 16 columns each)
         const uint32_t dst = sm100::smem_u32(out_r) + row * 128;
@@ -215,11 +197,11 @@ fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (BF16)
-                q[i] = pack4(__fmul_rn(bf16_lo(w[2 * i]), r), __fmul_rn(bf16_hi(w[2 * i]), r),
-                             __fmul_rn(bf16_lo(w[2 * i + 1]), r), __fmul_rn(bf16_hi(w[2 * i + 1]), r));
+                q[i] = fp8_codes4(make_float2(bf16_lo(w[2 * i]), bf16_hi(w[2 * i])),
+                                  make_float2(bf16_lo(w[2 * i + 1]), bf16_hi(w[2 * i + 1])), b);
             else
-                q[i] = pack4(__fmul_rn(__uint_as_float(w[4 * i]), r), __fmul_rn(__uint_as_float(w[4 * i + 1]), r),
-                             __fmul_rn(__uint_as_float(w[4 * i + 2]), r), __fmul_rn(__uint_as_float(w[4 * i + 3]), r));
+                q[i] = fp8_codes4(make_float2(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1])),
+                                  make_float2(__uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3])), b);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -232,7 +214,7 @@ fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid
     }
     if (COLS) {
         load_col();
-        float r0 = tile_r, r1 = tile_r;
+        Fp8Block b0 = tile, b1 = tile;
         if (LINES == 1) {
             float lo, hi;
             max_words(lo, hi);
@@ -245,13 +227,12 @@ fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid
                 m0 = fmaxf(m0, part[i * TILE + ccol]);
                 if (BF16) m1 = fmaxf(m1, part[i * TILE + ccol + 1]);
             }
-            const float s0 = scale_of(m0), s1 = scale_of(m1);
-            r0 = __frcp_rn(s0);
-            r1 = __frcp_rn(s1);
+            b0 = fp8_block(m0);
+            if (BF16) b1 = fp8_block(m1);
             if (rgroup == 0) {
                 float* sc = p.scales_cols + (int64_t)tr * p.lp_cols + col0 + ccol;
-                if (col0 + ccol < p.cols) sc[0] = s0;
-                if (BF16 && col0 + ccol + 1 < p.cols) sc[1] = s1;
+                if (col0 + ccol < p.cols) sc[0] = b0.s;
+                if (BF16 && col0 + ccol + 1 < p.cols) sc[1] = b1.s;
             }
         }
         const uint32_t dst = sm100::smem_u32(out_c);
@@ -263,13 +244,11 @@ fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid
             for (int e = 0; e < 4; ++e) {
                 const uint32_t* v = &w[16 * i + 4 * e];
                 if (BF16) {
-                    q0[e] = pack4(__fmul_rn(bf16_lo(v[0]), r0), __fmul_rn(bf16_lo(v[1]), r0),
-                                  __fmul_rn(bf16_lo(v[2]), r0), __fmul_rn(bf16_lo(v[3]), r0));
-                    q1[e] = pack4(__fmul_rn(bf16_hi(v[0]), r1), __fmul_rn(bf16_hi(v[1]), r1),
-                                  __fmul_rn(bf16_hi(v[2]), r1), __fmul_rn(bf16_hi(v[3]), r1));
+                    q0[e] = fp8_codes4(make_float2(bf16_lo(v[0]), bf16_lo(v[1])), make_float2(bf16_lo(v[2]), bf16_lo(v[3])), b0);
+                    q1[e] = fp8_codes4(make_float2(bf16_hi(v[0]), bf16_hi(v[1])), make_float2(bf16_hi(v[2]), bf16_hi(v[3])), b1);
                 } else {
-                    q0[e] = pack4(__fmul_rn(__uint_as_float(v[0]), r0), __fmul_rn(__uint_as_float(v[1]), r0),
-                                  __fmul_rn(__uint_as_float(v[2]), r0), __fmul_rn(__uint_as_float(v[3]), r0));
+                    q0[e] = fp8_codes4(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                       make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), b0);
                 }
             }
             if (BF16) {

@@ -460,8 +460,6 @@ cudaError_t run_pair(const Fp8GemmArgs& g, cudaStream_t s) {
 
 }  // namespace
 
-int64_t gemm_fp8_pair_tiles(int64_t M, int64_t N) { return ((M + PM - 1) / PM) * ((N + PN - 1) / PN); }
-
 cudaError_t launch_gemm_fp8_pair(const Fp8GemmArgs& g, cudaStream_t s) {
     if (g.b_lines == 1) return g.out_bf16 ? run_pair<true, true>(g, s) : run_pair<true, false>(g, s);
     return g.out_bf16 ? run_pair<false, true>(g, s) : run_pair<false, false>(g, s);

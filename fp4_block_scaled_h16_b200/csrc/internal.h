@@ -200,9 +200,8 @@ struct Fp8GemmArgs {
     int out_bf16;
     uint32_t wait_limit;
 };
-cudaError_t launch_gemm_fp8_split(const Fp8GemmArgs& g, cudaStream_t s);   // 128 lines x up to 128 rows, K over a cluster
+cudaError_t launch_gemm_fp8_split(const Fp8GemmArgs& g, cudaStream_t s);   // smaller tiles, K over a cluster
 cudaError_t launch_gemm_fp8_pair(const Fp8GemmArgs& g, cudaStream_t s);    // 256 x 256 tiles on CTA pairs
-int64_t gemm_fp8_pair_tiles(int64_t M, int64_t N);
 
 // the norms around a block with its gate and residual update (norm_residual.cu);
 // null pointers select what is left out

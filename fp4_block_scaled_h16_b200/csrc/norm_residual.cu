@@ -19,13 +19,17 @@
 // and y (8 B per element, 7 with FP8 codes for y), the backward call reads dy,
 // dhin, h' and o and writes dh' and do (12 B).  Every tensor crosses once: a
 // CTA holds a whole row in registers, 8 elements (16 bytes of bf16) per vector
-// and VPT vectors per thread, so the row statistics cost no second read.  All
-// sums are binary32; h' is rounded before its norm, because the stored h' is
-// what the next block and the backward call see.
+// and VPT vectors per thread, so the row statistics cost no second read, and the
+// next row's vectors are on their way while a row is worked on.  The products of
+// weights, gate and alpha that a column needs are kept in shared memory, where a
+// thread reads and writes only its own columns'.  All sums are binary32; h' is
+// rounded before its norm, because the stored h' is what the next block and the
+// backward call see.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "fp8_block.cuh"
 #include "internal.h"
 
 namespace fp4 {
@@ -33,61 +37,146 @@ namespace fp4 {
 namespace {
 
 constexpr int VEC = 8;                   // elements per vector
+constexpr int PAIRS = VEC / 2;
+
+// a vector as it is in memory: one (bf16) or two (fp32) 16-byte words
+template <bool BF16>
+struct Raw {
+    uint4 w[BF16 ? 1 : 2];
+};
+
+// the first `n` (1 .. 8) elements of a vector, the others zero
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_raw(const void* p, int n) {
+    Raw<BF16> r;
+    if (n >= VEC) {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.w[i] = static_cast<const uint4*>(p)[i];
+    } else {
+        uint32_t v[BF16 ? 4 : 8];
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 4 : 8); ++i) v[i] = 0u;
+#pragma unroll
+        for (int e = 0; e < VEC - 1; ++e)
+            if (e < n) {
+                if (BF16) v[e / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+                else v[BF16 ? 0 : e] = static_cast<const uint32_t*>(p)[e];
+            }
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.w[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    return r;
+}
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, int64_t row_off, int i, int cols, float (&v)[VEC]) {
-    const int c0 = VEC * i;
-    if (BF16) {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + row_off + c0;
-        if (c0 + VEC <= cols) {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-            v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
-        } else {
+__device__ __forceinline__ Raw<BF16> zero_raw() {
+    Raw<BF16> r;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = c0 + e < cols ? __bfloat162float(p[e]) : 0.0f;
-        }
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen(const Raw<BF16>& r, float2 (&v)[PAIRS]) {
+    if constexpr (BF16) {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
     } else {
-        const float* p = static_cast<const float*>(base) + row_off + c0;
-        if (c0 + VEC <= cols) {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = c0 + e < cols ? p[e] : 0.0f;
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = make_float2(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+            v[2 * i + 1] = make_float2(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
         }
     }
 }
 
+// rounded to the stored type (bf16: to nearest even)
 template <bool BF16>
-__device__ __forceinline__ void store8(void* base, int64_t row_off, int i, int cols, const float (&v)[VEC]) {
-    const int c0 = VEC * i;
-    if (BF16) {
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + row_off + c0;
-        if (c0 + VEC <= cols) {
-            uint32_t w[4];
+__device__ __forceinline__ Raw<BF16> narrow(const float2 (&v)[PAIRS]) {
+    Raw<BF16> r;
+    if constexpr (BF16) {
+        uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-                w[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (c0 + e < cols) p[e] = __float2bfloat16_rn(v[e]);
+        for (int i = 0; i < PAIRS; ++i) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[i].x, v[i].y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&x);
         }
+        r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-        float* p = static_cast<float*>(base) + row_off + c0;
-        if (c0 + VEC <= cols) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (c0 + e < cols) p[e] = v[e];
+        for (int i = 0; i < 2; ++i)
+            r.w[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
+                                __float_as_uint(v[2 * i + 1].y));
+    }
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_raw(void* p, int n, const Raw<BF16>& r) {
+    if (n >= VEC) {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) static_cast<uint4*>(p)[i] = r.w[i];
+    } else {
+        const uint32_t v[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[BF16 ? 0 : 1].x, r.w[BF16 ? 0 : 1].y,
+                               r.w[BF16 ? 0 : 1].z, r.w[BF16 ? 0 : 1].w};
+#pragma unroll
+        for (int e = 0; e < VEC - 1; ++e)
+            if (e < n) {
+                if (BF16) static_cast<uint16_t*>(p)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+                else static_cast<uint32_t*>(p)[e] = v[e];
+            }
+    }
+}
+
+// A float per column in shared memory, a thread's vector as two 16-byte words a
+// whole plane apart, so that neighbouring threads meet no bank twice.
+struct Columns {
+    float4* at;             // [2][vectors of the CTA]
+    int stride;             // vectors of the CTA
+    __device__ __forceinline__ void get(int i, float2 (&v)[PAIRS]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 w = at[h * stride + i];
+            v[2 * h] = make_float2(w.x, w.y);
+            v[2 * h + 1] = make_float2(w.z, w.w);
         }
+    }
+    __device__ __forceinline__ void set(int i, const float2 (&v)[PAIRS]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            at[h * stride + i] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
+    }
+};
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// byte address of vector i of a row that starts `row_off` elements into p
+template <bool BF16>
+__device__ __forceinline__ const void* vec_at(const void* p, int64_t row_off, int i) {
+    return static_cast<const char*>(p) + (row_off + (int64_t)VEC * i) * (BF16 ? 2 : 4);
+}
+template <bool BF16>
+__device__ __forceinline__ void* vec_at(void* p, int64_t row_off, int i) {
+    return static_cast<char*>(p) + (row_off + (int64_t)VEC * i) * (BF16 ? 2 : 4);
+}
+
+// the factor alpha g w_post of a vector's columns for gate row `grp`
+template <bool BF16>
+__device__ __forceinline__ void branch_factor(const void* w_post, const void* gate, int64_t ldg, float alpha,
+                                              int64_t grp, int i, int n, float2 (&f)[PAIRS]) {
+#pragma unroll
+    for (int e = 0; e < PAIRS; ++e) f[e] = both(alpha);
+    float2 v[PAIRS];
+    if (w_post) {
+        widen<BF16>(load_raw<BF16>(vec_at<BF16>(w_post, 0, i), n), v);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], v[e]);
+    }
+    if (gate) {
+        widen<BF16>(load_raw<BF16>(vec_at<BF16>(gate, grp * ldg, i), n), v);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], v[e]);
     }
 }
 
@@ -116,27 +205,67 @@ __device__ __forceinline__ float rstd_of(float sum, float cols, float eps) {
     return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, cols), eps)));
 }
 
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 256 : 512)
+// POST: the block output is normalised; RES: there is one
+template <bool BF16, int VPT, bool RES, bool POST>
+__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 4 : 1)
 norm_residual_kernel(const NormArgs a) {
+    extern __shared__ float4 columns[];
     __shared__ float part[2][1][32];
-    const int T = (int)blockDim.x, cols = (int)a.cols;
+    const int T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT;
+    const Columns w_pre{columns, vecs}, factor{columns + 2 * vecs, vecs};
+    int n[VPT];                               // elements of this thread's vectors inside the row
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) n[k] = cols - VEC * ((int)threadIdx.x + k * T);
+    if (a.w_pre) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int i = (int)threadIdx.x + k * T;
+            float2 v[PAIRS];
+            if (n[k] > 0) widen<BF16>(load_raw<BF16>(vec_at<BF16>(a.w_pre, 0, i), n[k]), v);
+            if (n[k] > 0) w_pre.set(i, v);
+        }
+    }
+    Raw<BF16> hr[VPT], orw[VPT];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int i = (int)threadIdx.x + k * T;
+            hr[k] = n[k] > 0 ? load_raw<BF16>(vec_at<BF16>(a.h, row * a.ldh, i), n[k]) : zero_raw<BF16>();
+            if (RES) orw[k] = n[k] > 0 ? load_raw<BF16>(vec_at<BF16>(a.o, row * a.ldo, i), n[k]) : zero_raw<BF16>();
+        }
+    };
+    int64_t grp = -1;
     int turn = 0;
+    if ((int64_t)blockIdx.x < a.rows) fetch(blockIdx.x);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float h[VPT][VEC];
+        float2 h[VPT][PAIRS], o[VPT][PAIRS];
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) load8<BF16>(a.h, row * a.ldh, (int)threadIdx.x + k * T, cols, h[k]);
-        if (a.o) {
-            float o[VPT][VEC];
+        for (int k = 0; k < VPT; ++k) {
+            widen<BF16>(hr[k], h[k]);
+            if (RES) widen<BF16>(orw[k], o[k]);
+        }
+        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        if (RES) {
+            const int64_t g = a.gate ? row / a.per : 0;
+            if (g != grp) {
+                grp = g;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) load8<BF16>(a.o, row * a.ldo, (int)threadIdx.x + k * T, cols, o[k]);
+                for (int k = 0; k < VPT; ++k) {
+                    const int i = (int)threadIdx.x + k * T;
+                    float2 f[PAIRS];
+                    if (n[k] <= 0) continue;
+                    branch_factor<BF16>(a.w_post, a.gate, a.ldg, a.alpha, grp, i, n[k], f);
+                    factor.set(i, f);
+                }
+            }
             float rstd = 1.0f;
-            if (a.w_post) {
-                float ss[1] = {0.0f};
+            if (POST) {
+                float2 s2 = both(0.0f);
 #pragma unroll
                 for (int k = 0; k < VPT; ++k)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) ss[0] = fmaf(o[k][e], o[k][e], ss[0]);
+                    for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(o[k][e], o[k][e], s2);
+                float ss[1] = {s2.x + s2.y};
                 block_sum<1>(ss, part[turn]);
                 turn ^= 1;
                 rstd = rstd_of(ss[0], (float)cols, a.eps);
@@ -145,32 +274,26 @@ norm_residual_kernel(const NormArgs a) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int i = (int)threadIdx.x + k * T;
-                if (VEC * i >= cols) continue;
-                float w[VEC];
-                if (a.w_post) {
-                    load8<BF16>(a.w_post, 0, i, cols, w);
+                if (n[k] <= 0) continue;
+                float2 f[PAIRS];
+                factor.get(i, f);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) o[k][e] = o[k][e] * rstd * w[e];
+                for (int e = 0; e < PAIRS; ++e) {
+                    if (POST) o[k][e] = __fmul2_rn(o[k][e], both(rstd));
+                    h[k][e] = __ffma2_rn(o[k][e], f[e], h[k][e]);
                 }
-                if (a.gate) {
-                    load8<BF16>(a.gate, row / a.per * a.ldg, i, cols, w);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) o[k][e] *= w[e];
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    h[k][e] = fmaf(a.alpha, o[k][e], h[k][e]);
-                    if (BF16) h[k][e] = __bfloat162float(__float2bfloat16_rn(h[k][e]));
-                }
-                store8<BF16>(a.h_out, row * a.ldho, i, cols, h[k]);
+                const Raw<BF16> r = narrow<BF16>(h[k]);
+                store_raw<BF16>(vec_at<BF16>(a.h_out, row * a.ldho, i), n[k], r);
+                if (BF16) widen<BF16>(r, h[k]);
             }
         }
         if (!a.w_pre) continue;
-        float ss[1] = {0.0f};
+        float2 s2 = both(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) ss[0] = fmaf(h[k][e], h[k][e], ss[0]);
+            for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(h[k][e], h[k][e], s2);
+        float ss[1] = {s2.x + s2.y};
         block_sum<1>(ss, part[turn]);
         turn ^= 1;
         const float rstd = rstd_of(ss[0], (float)cols, a.eps);
@@ -178,37 +301,39 @@ norm_residual_kernel(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int i = (int)threadIdx.x + k * T;
-            const bool live = VEC * i < cols;
-            float y[VEC];
-            if (live) load8<BF16>(a.w_pre, 0, i, cols, y);
+            const bool live = n[k] > 0;
+            // y = RN(RN(h' w) rstd): for bf16 the first product is exact
+            float2 t[PAIRS], f[PAIRS];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = live ? h[k][e] * rstd * y[e] : 0.0f;
-            if (a.y && live) store8<BF16>(a.y, row * a.ldy, i, cols, y);
+            for (int e = 0; e < PAIRS; ++e) f[e] = both(0.0f);
+            if (live) w_pre.get(i, f);
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) t[e] = __fmul2_rn(h[k][e], f[e]);
+            if (a.y && live) {
+                float2 y[PAIRS];
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) y[e] = __fmul2_rn(t[e], both(rstd));
+                store_raw<BF16>(vec_at<BF16>(a.y, row * a.ldy, i), n[k], narrow<BF16>(y));
+            }
             if (a.codes) {
-                // a block of 128 columns is 16 lanes' vectors
+                // a block of 128 columns is 16 lanes' vectors; its codes follow from
+                // h' w alone, because rstd is common to the block
                 float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) m = fmaxf(m, fabsf(y[e]));
+                for (int e = 0; e < PAIRS; ++e) m = fmaxf(m, fmaxf(fabsf(t[e].x), fabsf(t[e].y)));
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                float s = __fdiv_rn(m, 448.0f);
-                s = s >= 1.17549435e-38f ? s : 1.0f;
-                const float r = __frcp_rn(s);
+                const Fp8Block b = fp8_block(m, rstd);
                 if (live) {
-                    if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(i >> 4) * a.lp + row] = s;
-                    uint16_t q[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-                            : "=h"(q[e]) : "f"(__fmul_rn(y[2 * e + 1], r)), "f"(__fmul_rn(y[2 * e], r)));
+                    if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(i >> 4) * a.lp + row] = b.s;
+                    const uint2 q = make_uint2(fp8_codes4(t[0], t[1], b), fp8_codes4(t[2], t[3], b));
                     uint8_t* dst = a.codes + row * a.ldc + VEC * i;
-                    if (VEC * i + VEC <= cols) {
-                        *reinterpret_cast<uint2*>(dst) = make_uint2((uint32_t)q[0] | ((uint32_t)q[1] << 16),
-                                                                    (uint32_t)q[2] | ((uint32_t)q[3] << 16));
+                    if (n[k] >= VEC) {
+                        *reinterpret_cast<uint2*>(dst) = q;
                     } else {
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (VEC * i + e < cols) dst[e] = (uint8_t)(q[e >> 1] >> (8 * (e & 1)));
+                        for (int e = 0; e < VEC - 1; ++e)
+                            if (e < n[k]) dst[e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
                     }
                 }
             }
@@ -218,123 +343,191 @@ norm_residual_kernel(const NormArgs a) {
 
 // ------------------------------------------------------------------ backward
 
-// One CTA takes work items in turn: a run of rows inside one gate group, whose
-// dgate sums end with the item.  The sums for dw_pre and dw_post run over all
-// of a CTA's items.  Partial sums go to the workspace and are added in a fixed
-// order by norm_reduce_kernel, so results do not depend on timing.
+// One CTA takes work items in turn: a run of rows inside one gate group.  Over
+// an item it sums T = sum dh' n1 per column (n1 = o without w_post), from which
+// at its end both dgate = alpha w_post T and dw_post's share, alpha g T, follow.
+// dw_pre and dw_post run over all of a CTA's items.  Partial sums go to the
+// workspace and are added in a fixed order by norm_reduce_kernel, so results do
+// not depend on timing.
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 256 : 512)
+__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 2 : 1)
 norm_residual_backward_kernel(const NormBwdArgs a) {
+    extern __shared__ float4 columns[];
     __shared__ float part[2][3][32];
-    const int T = (int)blockDim.x, cols = (int)a.cols;
+    const int T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT;
+    const Columns w_pre{columns, vecs}, factor{columns + 2 * vecs, vecs}, post{columns + 4 * vecs, vecs};
     const float inv_cols = 1.0f / (float)cols;
+    int n[VPT];
+    float2 acc_pre[VPT][PAIRS];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int i = (int)threadIdx.x + k * T;
+        n[k] = cols - VEC * i;
+        float2 v[PAIRS];
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) acc_pre[k][e] = v[e] = both(0.0f);
+        post.set(i, v);
+        if (a.w_pre && n[k] > 0) {
+            widen<BF16>(load_raw<BF16>(vec_at<BF16>(a.w_pre, 0, i), n[k]), v);
+            w_pre.set(i, v);
+        }
+    }
+    Raw<BF16> r_dhin[VPT], r_dy[VPT], r_h[VPT], r_o[VPT];
+    float rstd2n = 0.0f, rstd1n = 1.0f;
+    auto fetch = [&](int64_t row) {
+        if (a.w_pre) rstd2n = a.rstd_pre[row];
+        if (a.w_post) rstd1n = a.rstd_post[row];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int i = (int)threadIdx.x + k * T;
+            r_dhin[k] = r_dy[k] = r_h[k] = r_o[k] = zero_raw<BF16>();
+            if (n[k] <= 0) continue;
+            if (a.dh_in) r_dhin[k] = load_raw<BF16>(vec_at<BF16>(a.dh_in, row * a.lddhi, i), n[k]);
+            if (a.w_pre) {
+                r_dy[k] = load_raw<BF16>(vec_at<BF16>(a.dy, row * a.lddy, i), n[k]);
+                r_h[k] = load_raw<BF16>(vec_at<BF16>(a.h, row * a.ldh, i), n[k]);
+            }
+            if (a.o) r_o[k] = load_raw<BF16>(vec_at<BF16>(a.o, row * a.ldo, i), n[k]);
+        }
+    };
+    // the rows of item `it`
+    auto bounds = [&](int64_t it, int64_t& grp, int64_t& first, int64_t& last) {
+        grp = it / a.nseg;
+        first = grp * a.per + (it - grp * a.nseg) * a.seg_rows;
+        last = min(min(first + a.seg_rows, (grp + 1) * a.per), a.rows);
+    };
     int turn = 0;
-    float acc_pre[VPT][VEC], acc_post[VPT][VEC];
+    int64_t grp = 0, row = 0, last = 0;
+    int64_t item = blockIdx.x;
+    if (item < a.items) {
+        bounds(item, grp, row, last);
+        if (row < last) fetch(row);
+    }
+    for (; item < a.items; item += gridDim.x) {
+        int64_t grp_next = 0, row_next = 0, last_next = 0;
+        if (item + gridDim.x < a.items) bounds(item + gridDim.x, grp_next, row_next, last_next);
+        float2 acc[VPT][PAIRS];                    // sum dh' n1
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) {
+            const int i = (int)threadIdx.x + k * T;
+            float2 f[PAIRS];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc_pre[k][e] = acc_post[k][e] = 0.0f;
-    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-        const int64_t grp = item / a.nseg, seg = item % a.nseg;
-        const int64_t first = grp * a.per + seg * a.seg_rows;
-        int64_t last = first + a.seg_rows;
-        if (last > (grp + 1) * a.per) last = (grp + 1) * a.per;
-        if (last > a.rows) last = a.rows;
-        float acc_gate[VPT][VEC];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) acc_gate[k][e] = 0.0f;
-        for (int64_t row = first; row < last; ++row) {
-            const float rstd2 = a.w_pre ? a.rstd_pre[row] : 0.0f, rstd1 = a.w_post ? a.rstd_post[row] : 1.0f;
-            // A = dhin + rstd2 dy w_pre, n2, o and u = alpha g w_post n1: with
-            // dh' = A - rstd2 n2 c1, both means follow from three sums of one pass:
-            // c1 = mean(a n2), c2 = mean(b n1) = mean(u A) - c1 mean(u rstd2 n2)
-            float A[VPT][VEC], n2[VPT][VEC], o[VPT][VEC];
-            float sums[3] = {0.0f, 0.0f, 0.0f};
+            for (int e = 0; e < PAIRS; ++e) acc[k][e] = both(0.0f);
+            if (n[k] <= 0 || !a.o) continue;
+            branch_factor<BF16>(a.w_post, a.gate, a.ldg, a.alpha, grp, i, n[k], f);
+            factor.set(i, f);
+        }
+        for (; row < last; ++row) {
+            const float rstd2 = rstd2n, rstd1 = rstd1n;
+            // A = dhin + rstd2 a, n2, n1 and u = alpha g w_post n1: with dh' = A -
+            // rstd2 n2 c1, both means follow from three sums of one pass:
+            // c1 = mean(a n2), c2 = mean(b n1) = mean(u A) - c1 rstd2 mean(u n2)
+            float2 A[VPT][PAIRS], n2[VPT][PAIRS], n1[VPT][PAIRS];
+            float2 s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int i = (int)threadIdx.x + k * T;
+                widen<BF16>(r_dhin[k], A[k]);
+                widen<BF16>(r_h[k], n2[k]);
+                widen<BF16>(r_o[k], n1[k]);
+                if (a.w_pre && n[k] > 0) {
+                    float2 dy[PAIRS], w[PAIRS];
+                    widen<BF16>(r_dy[k], dy);
+                    w_pre.get(i, w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) A[k][e] = n2[k][e] = o[k][e] = 0.0f;
-                if (VEC * i >= cols) continue;
-                if (a.dh_in) load8<BF16>(a.dh_in, row * a.lddhi, i, cols, A[k]);
-                if (a.o) load8<BF16>(a.o, row * a.ldo, i, cols, o[k]);
-                if (a.w_pre) {
-                    float dy[VEC], w[VEC];
-                    load8<BF16>(a.dy, row * a.lddy, i, cols, dy);
-                    load8<BF16>(a.h, row * a.ldh, i, cols, n2[k]);
-                    load8<BF16>(a.w_pre, 0, i, cols, w);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        n2[k][e] *= rstd2;
-                        acc_pre[k][e] = fmaf(dy[e], n2[k][e], acc_pre[k][e]);
-                        const float d = dy[e] * w[e];
-                        sums[0] = fmaf(d, n2[k][e], sums[0]);
-                        A[k][e] = fmaf(rstd2, d, A[k][e]);
+                    for (int e = 0; e < PAIRS; ++e) {
+                        n2[k][e] = __fmul2_rn(n2[k][e], both(rstd2));
+                        acc_pre[k][e] = __ffma2_rn(dy[e], n2[k][e], acc_pre[k][e]);
+                        const float2 d = __fmul2_rn(dy[e], w[e]);
+                        s0 = __ffma2_rn(d, n2[k][e], s0);
+                        A[k][e] = __ffma2_rn(d, both(rstd2), A[k][e]);
                     }
                 }
-                if (a.w_post) {
-                    float w[VEC], g[VEC];
-                    load8<BF16>(a.w_post, 0, i, cols, w);
-                    if (a.gate) load8<BF16>(a.gate, grp * a.ldg, i, cols, g);
+                if (a.w_post && n[k] > 0) {
+                    float2 f[PAIRS];
+                    factor.get(i, f);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float u = a.alpha * (a.gate ? g[e] : 1.0f) * w[e] * (o[k][e] * rstd1);
-                        sums[1] = fmaf(u, A[k][e], sums[1]);
-                        sums[2] = fmaf(u, rstd2 * n2[k][e], sums[2]);
+                    for (int e = 0; e < PAIRS; ++e) {
+                        n1[k][e] = __fmul2_rn(n1[k][e], both(rstd1));
+                        const float2 u = __fmul2_rn(f[e], n1[k][e]);
+                        s1 = __ffma2_rn(u, A[k][e], s1);
+                        s2 = __ffma2_rn(u, n2[k][e], s2);
                     }
                 }
             }
-            block_sum<3>(sums, part[turn]);
-            turn ^= 1;
-            const float c1 = sums[0] * inv_cols, c2 = (sums[1] - c1 * sums[2]) * inv_cols;
+            if (row + 1 < last) fetch(row + 1);
+            else if (row_next < last_next) fetch(row_next);
+            float c1 = 0.0f, c2 = 0.0f;
+            if (a.w_pre || a.w_post) {
+                float sums[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+                block_sum<3>(sums, part[turn]);
+                turn ^= 1;
+                c1 = rstd2 * (sums[0] * inv_cols);
+                c2 = (sums[1] - c1 * sums[2]) * inv_cols;
+            }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int i = (int)threadIdx.x + k * T;
-                if (VEC * i >= cols) continue;
-                float dh[VEC];
+                if (n[k] <= 0) continue;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) dh[e] = fmaf(-rstd2 * c1, n2[k][e], A[k][e]);
-                store8<BF16>(a.dh, row * a.lddh, i, cols, dh);
+                for (int e = 0; e < PAIRS; ++e) A[k][e] = __ffma2_rn(n2[k][e], both(-c1), A[k][e]);      // dh'
+                store_raw<BF16>(vec_at<BF16>(a.dh, row * a.lddh, i), n[k], narrow<BF16>(A[k]));
                 if (!a.o) continue;
-                float w[VEC], g[VEC], d[VEC];
-                if (a.w_post) load8<BF16>(a.w_post, 0, i, cols, w);
-                if (a.gate) load8<BF16>(a.gate, grp * a.ldg, i, cols, g);
+                float2 f[PAIRS];
+                factor.get(i, f);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float dr = a.alpha * dh[e], gr = a.gate ? g[e] * dr : dr;
-                    const float n1 = o[k][e] * rstd1;
-                    if (a.gate) acc_gate[k][e] = fmaf(dr, a.w_post ? n1 * w[e] : o[k][e], acc_gate[k][e]);
-                    if (a.w_post) {
-                        acc_post[k][e] = fmaf(gr, n1, acc_post[k][e]);
-                        d[e] = rstd1 * (gr * w[e] - n1 * c2);
-                    } else {
-                        d[e] = gr;
-                    }
+                for (int e = 0; e < PAIRS; ++e) {
+                    acc[k][e] = __ffma2_rn(A[k][e], n1[k][e], acc[k][e]);
+                    f[e] = __fmul2_rn(A[k][e], f[e]);                                    // b, or do itself
+                    if (a.w_post) f[e] = __fmul2_rn(__ffma2_rn(n1[k][e], both(-c2), f[e]), both(rstd1));
                 }
-                store8<BF16>(a.d_o, row * a.lddo, i, cols, d);
+                store_raw<BF16>(vec_at<BF16>(a.d_o, row * a.lddo, i), n[k], narrow<BF16>(f));
             }
         }
-        if (a.gate) {
+        if (a.gate || a.w_post) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int i = (int)threadIdx.x + k * T;
-                if (a.gate_pitch % 4 == 0) {
-                    store8<false>(a.gate_part, item * a.gate_pitch, i, cols, acc_gate[k]);
-                } else {                 // dgate itself, with an odd row pitch
+                if (n[k] <= 0) continue;
+                float2 f[PAIRS];
+                if (a.w_post) {
+                    float2 p[PAIRS];
+                    branch_factor<BF16>(nullptr, a.gate, a.ldg, a.alpha, grp, i, n[k], f);
+                    post.get(i, p);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (VEC * i + e < cols) a.gate_part[item * a.gate_pitch + VEC * i + e] = acc_gate[k][e];
+                    for (int e = 0; e < PAIRS; ++e) p[e] = __ffma2_rn(f[e], acc[k][e], p[e]);
+                    post.set(i, p);
+                }
+                if (a.gate) {
+                    branch_factor<BF16>(a.w_post, nullptr, 0, a.alpha, 0, i, n[k], f);
+#pragma unroll
+                    for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], acc[k][e]);
+                    float* dst = a.gate_part + item * a.gate_pitch + VEC * i;
+                    if (a.gate_pitch % 4 == 0) {
+                        store_raw<false>(dst, n[k], narrow<false>(f));
+                    } else {                 // dgate itself, with an odd row pitch
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (e < n[k]) dst[e] = (e & 1) ? f[e / 2].y : f[e / 2].x;
+                    }
                 }
             }
         }
+        grp = grp_next;
+        row = row_next;
+        last = last_next;
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int i = (int)threadIdx.x + k * T;
-        if (a.w_pre) store8<false>(a.pre_part, (int64_t)blockIdx.x * a.pitch, i, cols, acc_pre[k]);
-        if (a.w_post) store8<false>(a.post_part, (int64_t)blockIdx.x * a.pitch, i, cols, acc_post[k]);
+        if (n[k] <= 0) continue;
+        const int64_t at = (int64_t)blockIdx.x * a.pitch + VEC * i;
+        if (a.w_pre) store_raw<false>(a.pre_part + at, n[k], narrow<false>(acc_pre[k]));
+        if (a.w_post) {
+            float2 p[PAIRS];
+            post.get(i, p);
+            store_raw<false>(a.post_part + at, n[k], narrow<false>(p));
+        }
     }
 }
 
@@ -378,33 +571,48 @@ void shape_of(int64_t cols, int& vpt, int& threads) {
     threads = (int)(((nvec + vpt - 1) / vpt + 31) / 32 * 32);
 }
 
-template <bool BF16, int VPT>
+template <bool BF16, int VPT, bool RES, bool POST>
 cudaError_t run_norm(const NormArgs& a, int threads, cudaStream_t s) {
     static PerDeviceOnce setup;
     static int per_sm[kOnceDevices][17] = {};
+    const auto smem = [](int t) { return (size_t)t * VPT * VEC * sizeof(float) * (RES ? 2 : 1); };
     int dev = 0;
-    cudaError_t e = setup.run([](int d) {
-        for (int w = 1; w <= 16; ++w) {
+    const cudaError_t e = setup.run([&](int d) {
+        cudaError_t err = cudaFuncSetAttribute(norm_residual_kernel<BF16, VPT, RES, POST>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(512));
+        for (int w = 1; w <= (VPT == 1 ? 8 : 16) && err == cudaSuccess; ++w) {
             int n = 0;
-            const cudaError_t err =
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_residual_kernel<BF16, VPT>, 32 * w, 0);
-            if (err != cudaSuccess) return err;
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_residual_kernel<BF16, VPT, RES, POST>, 32 * w,
+                                                                smem(32 * w));
             per_sm[d][w] = n < 1 ? 1 : n;
         }
-        return cudaSuccess;
+        return err;
     }, &dev);
     if (e != cudaSuccess) return e;
     const int64_t cap = (int64_t)num_sms() * per_sm[dev][threads / 32];
     const unsigned grid = (unsigned)(a.rows < cap ? a.rows : cap);
-    norm_residual_kernel<BF16, VPT><<<grid, threads, 0, s>>>(a);
+    norm_residual_kernel<BF16, VPT, RES, POST><<<grid, threads, smem(threads), s>>>(a);
     return cudaGetLastError();
 }
 
 template <bool BF16, int VPT>
+cudaError_t run_norm_parts(const NormArgs& a, int threads, cudaStream_t s) {
+    if (!a.o) return run_norm<BF16, VPT, false, false>(a, threads, s);
+    return a.w_post ? run_norm<BF16, VPT, true, true>(a, threads, s) : run_norm<BF16, VPT, true, false>(a, threads, s);
+}
+
+template <bool BF16, int VPT>
 cudaError_t run_norm_bwd(const NormBwdArgs& a, int threads, cudaStream_t s) {
+    static PerDeviceOnce setup;
+    const auto smem = [](int t) { return (size_t)t * VPT * VEC * sizeof(float) * 3; };
+    cudaError_t e = setup.run([&](int) {
+        return cudaFuncSetAttribute(norm_residual_backward_kernel<BF16, VPT>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(512));
+    });
+    if (e != cudaSuccess) return e;
     const int ctas = (int)(a.items < NORM_BWD_CTAS ? a.items : NORM_BWD_CTAS);
-    norm_residual_backward_kernel<BF16, VPT><<<ctas, threads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    norm_residual_backward_kernel<BF16, VPT><<<ctas, threads, smem(threads), s>>>(a);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t jobs = (a.w_pre ? 1 : 0) + (a.w_post ? 1 : 0) + ((a.gate && a.nseg > 1) ? a.groups : 0);
     if (jobs == 0) return cudaSuccess;
@@ -436,9 +644,9 @@ cudaError_t launch_norm(const NormArgs& a, bool bf16, cudaStream_t s) {
     int vpt, threads;
     shape_of(a.cols, vpt, threads);
     switch (vpt) {
-    case 1: return bf16 ? run_norm<true, 1>(a, threads, s) : run_norm<false, 1>(a, threads, s);
-    case 2: return bf16 ? run_norm<true, 2>(a, threads, s) : run_norm<false, 2>(a, threads, s);
-    default: return bf16 ? run_norm<true, 4>(a, threads, s) : run_norm<false, 4>(a, threads, s);
+    case 1: return bf16 ? run_norm_parts<true, 1>(a, threads, s) : run_norm_parts<false, 1>(a, threads, s);
+    case 2: return bf16 ? run_norm_parts<true, 2>(a, threads, s) : run_norm_parts<false, 2>(a, threads, s);
+    default: return bf16 ? run_norm_parts<true, 4>(a, threads, s) : run_norm_parts<false, 4>(a, threads, s);
     }
 }
 

@@ -480,7 +480,9 @@ size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines);
  * transposed operand of Dgrad and Wgrad), or both from one read.  With m the
  * largest |x| of a block:
  *     s = RN(m / 448)  (1 where that is below the smallest normal binary32),
- *     r = RN(1 / s),   code = E4M3_rne_satfinite(RN(x r)).
+ *     code = E4M3_rne_satfinite(448 x / m)  (of x itself where s is 1 for that),
+ * the quotient taken in binary32: exactly rounded for bf16 inputs, within two
+ * units in the last place for fp32 inputs.
  *   x, in_dtype, rows, cols, ld   input, as fp4_quantize; any rows and cols
  *   block_lines     1 or 128
  *   codes_rows, ld_rows, scales_rows   the rows' result, or codes_rows NULL

@@ -455,8 +455,9 @@ def gemm_outctl(a: dict, b: dict):
 def fp8_block_quantize(x: np.ndarray, block_lines: int = 1, axis: int = 1) -> dict:
     """E4M3 with one FP32 scale per block of 128 elements along the lines, of
     block_lines lines: m = max|x|, s = RN(m / 448) (1 where that is below the
-    smallest normal binary32), r = RN(1 / s), code = E4M3(RN(x r)).  Returns
-    codes [L, K] and scales [L or ceil(L / 128), ceil(K / 128)]."""
+    smallest normal binary32), code = E4M3(RN(448 x / m)), of x itself where s
+    was replaced.  Returns codes [L, K], the quotients they were rounded from
+    and scales [L or ceil(L / 128), ceil(K / 128)]."""
     v = widen(np.ascontiguousarray(x))
     v = np.ascontiguousarray(v if axis == 1 else v.T)
     L, K = v.shape
@@ -468,15 +469,19 @@ def fp8_block_quantize(x: np.ndarray, block_lines: int = 1, axis: int = 1) -> di
         line_max = np.abs(part).max(axis=1) if L else np.zeros(0, np.float32)
         for b in range(nl):
             at = slice(b * block_lines, min(L, (b + 1) * block_lines))
-            s = np.float32(line_max[at].max() / np.float32(448.0))
-            if not s >= np.float32(2.0 ** -126):
+            m = line_max[at].max()
+            s = np.float32(m / np.float32(448.0))
+            if s >= np.float32(2.0 ** -126):
+                # the binary64 quotient rounded to binary32 is the rounded quotient (53 >= 2 * 24 + 2 bits)
+                scaled[at, 128 * k:128 * (k + 1)] = (448.0 * part[at].astype(np.float64) / np.float64(m)).astype(np.float32)
+            else:
                 s = np.float32(1.0)
+                scaled[at, 128 * k:128 * (k + 1)] = part[at]
             scales[b, k] = s
-            scaled[at, 128 * k:128 * (k + 1)] = part[at] * (np.float32(1.0) / s)
     codes = np.zeros((L, K), np.uint8)
     if scaled.size:
         lib().orc_fp8_encode_array(_ptr(scaled), scaled.size, 1.0, _ptr(codes))
-    return dict(codes=codes, scales=scales, block_lines=block_lines)
+    return dict(codes=codes, scales=scales, quotients=scaled, block_lines=block_lines)
 
 
 def fp8_block_dequantize(q: dict) -> np.ndarray:

@@ -1,5 +1,6 @@
-"""FP8 with a scale per block of 128 on the GPU against the oracle: codes and
-scales bit for bit, the GEMM within |C - C64| <= 1e-5 sum |a b| (+ half a bf16
+"""FP8 with a scale per block of 128 on the GPU against the oracle: scales and
+the codes of bf16 bit for bit, the codes of fp32 but for quotients within three
+roundings of the middle of two codes, the GEMM within |C - C64| <= 1e-5 sum |a b| (+ half a bf16
 step of the result for bf16 output), on both of its kernels.
 
 The GEMM's bound: a chunk's tensor-core sum of 128 products takes part in at
@@ -32,12 +33,21 @@ def make(rows, cols, seed, dtype=torch.bfloat16, pad=0):
     return torch.from_numpy(x).to(dtype)[:, :cols]
 
 
-def assert_same(fp4, q, o, what=""):
+def assert_same(q, o, exact, what=""):
     codes, scales = q["codes"].cpu().numpy()[:, :q["K"]], q["scales"].cpu().numpy()
     n = o["scales"].shape[0]
     assert (scales[:, :n].T.view(np.uint32) == o["scales"].view(np.uint32)).all(), what + " scales"
-    bad = np.argwhere(codes != o["codes"])
-    assert len(bad) == 0, "%s: %d codes differ, first %s" % (what, len(bad), bad[:3].tolist())
+    bad = codes != o["codes"]
+    if exact:
+        at = np.argwhere(bad)
+        assert len(at) == 0, "%s: %d codes differ, first %s" % (what, len(at), at[:3].tolist())
+    elif bad.any():
+        # 7 x is rounded, the corrected quotient is, and the oracle's is: three
+        # roundings of 2^-24 may lie between the two sides of the middle of two codes
+        value = lambda c: oracle.fp8_dequantize(dict(codes=c.reshape(1, -1), scale=1.0))[0]  # noqa: E731
+        got, want, quotient = codes[bad], o["codes"][bad], o["quotients"][bad].astype(np.float64)
+        assert (np.abs(got.astype(int) - want.astype(int)) == 1).all(), what
+        assert (np.abs(quotient - (value(got) + value(want)) / 2) <= 3 * 2.0 ** -24 * np.abs(quotient)).all(), what
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 130), (128, 128), (127, 129), (129, 127), (300, 513), (1000, 272), (257, 2000)]
@@ -55,11 +65,12 @@ def test_quantize_matches_oracle(fp4, dtype, lines, shape, pad):
         xd[:, shape[1]:] = 1e30                          # never read into a block
     xd = xd[:, :shape[1]]
     want = [oracle.fp8_block_quantize(oracle_input(x.contiguous()), lines, axis) for axis in (1, 0)]
-    assert_same(fp4, fp4.fp8_block_quantize(xd, 1, lines), want[0], "rows")
-    assert_same(fp4, fp4.fp8_block_quantize(xd, 0, lines), want[1], "columns")
+    exact = dtype == torch.bfloat16
+    assert_same(fp4.fp8_block_quantize(xd, 1, lines), want[0], exact, "rows")
+    assert_same(fp4.fp8_block_quantize(xd, 0, lines), want[1], exact, "columns")
     qr, qc = fp4.fp8_block_quantize_both_axes(xd, lines)
-    assert_same(fp4, qr, want[0], "rows of both")
-    assert_same(fp4, qc, want[1], "columns of both")
+    assert_same(qr, want[0], exact, "rows of both")
+    assert_same(qc, want[1], exact, "columns of both")
     assert fp4.fp4_last_error() == fp4.FP4_OK
 
 

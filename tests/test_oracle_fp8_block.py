@@ -26,9 +26,9 @@ def test_codes_and_scales_against_torch(shape, lines, axis):
     for b in range(-(-L // lines)):
         for k in range(-(-K // 128)):
             at = (slice(b * lines, min(L, (b + 1) * lines)), slice(128 * k, min(K, 128 * k + 128)))
-            s = np.float32(np.abs(v[at]).max()) / np.float32(448)
-            assert q["scales"][b, k] == s
-            assert (q["codes"][at] == e4m3_by_torch(v[at] * (np.float32(1) / s))).all()
+            m = np.abs(v[at]).max()
+            assert q["scales"][b, k] == np.float32(m) / np.float32(448)
+            assert (q["codes"][at] == e4m3_by_torch((448.0 * v[at].astype(np.float64) / m).astype(np.float32))).all()
 
 
 def test_block_maximum_takes_the_top_code_and_zeros_stay_zero():
@@ -44,6 +44,13 @@ def test_a_quotient_below_the_smallest_normal_gives_scale_one():
     x = np.full((1, 128), np.float32(2.0 ** -120))
     q = oracle.fp8_block_quantize(x)
     assert q["scales"][0, 0] == 1 and (q["codes"] == 0).all()
+
+
+def test_a_quotient_in_the_middle_of_two_codes_goes_to_the_even_one():
+    # m = 7 / 4: 448 x / m = 256 x; 17/16 * 256 = 272 lies between 256 (0x78) and 288 (0x79)
+    x = np.zeros((1, 128), np.float32)
+    x[0, :3] = 1.75, 17 / 16, 19 / 16                     # 304: between 288 (0x79) and 320 (0x7A)
+    assert oracle.fp8_block_quantize(x)["codes"][0, :3].tolist() == [0x7E, 0x78, 0x7A]
 
 
 def test_values_that_e4m3_holds_come_back_exactly():
