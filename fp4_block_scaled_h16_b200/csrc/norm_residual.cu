@@ -151,87 +151,105 @@ struct Columns {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// byte address of vector i of a row that starts `row_off` elements into p
+// a row that starts `row_off` elements into p, the same for the whole CTA, and
+// in it the vector at byte `off`
 template <bool BF16>
-__device__ __forceinline__ const void* vec_at(const void* p, int64_t row_off, int i) {
-    return static_cast<const char*>(p) + (row_off + (int64_t)VEC * i) * (BF16 ? 2 : 4);
+__device__ __forceinline__ const char* row_at(const void* p, int64_t row_off) {
+    return static_cast<const char*>(p) + row_off * (BF16 ? 2 : 4);
 }
 template <bool BF16>
-__device__ __forceinline__ void* vec_at(void* p, int64_t row_off, int i) {
-    return static_cast<char*>(p) + (row_off + (int64_t)VEC * i) * (BF16 ? 2 : 4);
+__device__ __forceinline__ char* row_at(void* p, int64_t row_off) {
+    return static_cast<char*>(p) + row_off * (BF16 ? 2 : 4);
 }
 
 // the factor alpha g w_post of a vector's columns for gate row `grp`
 template <bool BF16>
 __device__ __forceinline__ void branch_factor(const void* w_post, const void* gate, int64_t ldg, float alpha,
-                                              int64_t grp, int i, int n, float2 (&f)[PAIRS]) {
+                                              int64_t grp, uint32_t off, int n, float2 (&f)[PAIRS]) {
 #pragma unroll
     for (int e = 0; e < PAIRS; ++e) f[e] = both(alpha);
     float2 v[PAIRS];
     if (w_post) {
-        widen<BF16>(load_raw<BF16>(vec_at<BF16>(w_post, 0, i), n), v);
+        widen<BF16>(load_raw<BF16>(row_at<BF16>(w_post, 0) + off, n), v);
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], v[e]);
     }
     if (gate) {
-        widen<BF16>(load_raw<BF16>(vec_at<BF16>(gate, grp * ldg, i), n), v);
+        widen<BF16>(load_raw<BF16>(row_at<BF16>(gate, grp * ldg) + off, n), v);
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], v[e]);
     }
 }
 
-// sums of N values over the CTA, in a fixed order; every thread gets them.
-// `part` alternates between two buffers from call to call, so one barrier is enough.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[32]) {
+// sums of up to four values over the CTA, in a fixed order; every thread gets
+// them.  `part` alternates between two buffers from call to call, so one barrier
+// is enough.
+__device__ __forceinline__ float4 block_sum(float4 v, float4* part, int tid, int warps) {
+    float2 lo = make_float2(v.x, v.y), hi = make_float2(v.z, v.w);
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], d);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
-    if (lane == 0)
-#pragma unroll
-        for (int n = 0; n < N; ++n) part[n][warp] = v[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        float s = 0.0f;
-        for (int w = 0; w < warps; ++w) s += part[n][w];
-        v[n] = s;
+    for (int d = 16; d > 0; d >>= 1) {
+        lo = __fadd2_rn(lo, make_float2(__shfl_xor_sync(0xffffffffu, lo.x, d), __shfl_xor_sync(0xffffffffu, lo.y, d)));
+        hi.x += __shfl_xor_sync(0xffffffffu, hi.x, d);
     }
+    if ((tid & 31) == 0) part[tid >> 5] = make_float4(lo.x, lo.y, hi.x, 0.0f);
+    __syncthreads();
+    float4 s = part[0];
+    lo = make_float2(s.x, s.y);
+    for (int w = 1; w < warps; ++w) {
+        const float4 t = part[w];
+        lo = __fadd2_rn(lo, make_float2(t.x, t.y));
+        s.z += t.z;
+    }
+    return make_float4(lo.x, lo.y, s.z, 0.0f);
+}
+__device__ __forceinline__ float block_sum(float v, float* part, int tid, int warps) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if ((tid & 31) == 0) part[tid >> 5] = v;
+    __syncthreads();
+    float s = part[0];
+    for (int w = 1; w < warps; ++w) s += part[w];
+    return s;
 }
 
 __device__ __forceinline__ float rstd_of(float sum, float cols, float eps) {
     return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, cols), eps)));
 }
 
-// POST: the block output is normalised; RES: there is one
-template <bool BF16, int VPT, bool RES, bool POST>
-__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 4 : 1)
+// FULL: the row is exactly the CTA's vectors, none of them partial or empty.
+// POST: the block output is normalised; RES: there is one.
+template <bool BF16, int VPT, int THREADS, bool FULL, bool RES, bool POST>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : (VPT == 1 ? 4 : 3))
 norm_residual_kernel(const NormArgs a) {
+    constexpr uint32_t BYTES = VEC * (BF16 ? 2 : 4);
     extern __shared__ float4 columns[];
-    __shared__ float part[2][1][32];
-    const int T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT;
+    __shared__ float part[2][32];
+    const int tid = (int)threadIdx.x, T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT, warps = T >> 5;
     const Columns w_pre{columns, vecs}, factor{columns + 2 * vecs, vecs};
     int n[VPT];                               // elements of this thread's vectors inside the row
+    uint32_t off[VPT];                        // and where they start
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) n[k] = cols - VEC * ((int)threadIdx.x + k * T);
+    for (int k = 0; k < VPT; ++k) {
+        n[k] = FULL ? VEC : cols - VEC * (tid + k * T);
+        off[k] = BYTES * (uint32_t)(tid + k * T);
+    }
     if (a.w_pre) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = (int)threadIdx.x + k * T;
+            if (n[k] <= 0) continue;
             float2 v[PAIRS];
-            if (n[k] > 0) widen<BF16>(load_raw<BF16>(vec_at<BF16>(a.w_pre, 0, i), n[k]), v);
-            if (n[k] > 0) w_pre.set(i, v);
+            widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), v);
+            w_pre.set(tid + k * T, v);
         }
     }
     Raw<BF16> hr[VPT], orw[VPT];
     auto fetch = [&](int64_t row) {
+        const char* h = row_at<BF16>(a.h, row * a.ldh);
+        const char* o = row_at<BF16>(a.o, row * a.ldo);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = (int)threadIdx.x + k * T;
-            hr[k] = n[k] > 0 ? load_raw<BF16>(vec_at<BF16>(a.h, row * a.ldh, i), n[k]) : zero_raw<BF16>();
-            if (RES) orw[k] = n[k] > 0 ? load_raw<BF16>(vec_at<BF16>(a.o, row * a.ldo, i), n[k]) : zero_raw<BF16>();
+            hr[k] = n[k] > 0 ? load_raw<BF16>(h + off[k], n[k]) : zero_raw<BF16>();
+            if (RES) orw[k] = n[k] > 0 ? load_raw<BF16>(o + off[k], n[k]) : zero_raw<BF16>();
         }
     };
     int64_t grp = -1;
@@ -251,11 +269,10 @@ norm_residual_kernel(const NormArgs a) {
                 grp = g;
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
-                    const int i = (int)threadIdx.x + k * T;
                     float2 f[PAIRS];
                     if (n[k] <= 0) continue;
-                    branch_factor<BF16>(a.w_post, a.gate, a.ldg, a.alpha, grp, i, n[k], f);
-                    factor.set(i, f);
+                    branch_factor<BF16>(a.w_post, a.gate, a.ldg, a.alpha, grp, off[k], n[k], f);
+                    factor.set(tid + k * T, f);
                 }
             }
             float rstd = 1.0f;
@@ -265,25 +282,23 @@ norm_residual_kernel(const NormArgs a) {
                 for (int k = 0; k < VPT; ++k)
 #pragma unroll
                     for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(o[k][e], o[k][e], s2);
-                float ss[1] = {s2.x + s2.y};
-                block_sum<1>(ss, part[turn]);
+                rstd = rstd_of(block_sum(s2.x + s2.y, part[turn], tid, warps), (float)cols, a.eps);
                 turn ^= 1;
-                rstd = rstd_of(ss[0], (float)cols, a.eps);
-                if (threadIdx.x == 0) a.rstd_post[row] = rstd;
+                if (tid == 0) a.rstd_post[row] = rstd;
             }
+            char* h_out = row_at<BF16>(a.h_out, row * a.ldho);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int i = (int)threadIdx.x + k * T;
                 if (n[k] <= 0) continue;
                 float2 f[PAIRS];
-                factor.get(i, f);
+                factor.get(tid + k * T, f);
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
                     if (POST) o[k][e] = __fmul2_rn(o[k][e], both(rstd));
                     h[k][e] = __ffma2_rn(o[k][e], f[e], h[k][e]);
                 }
                 const Raw<BF16> r = narrow<BF16>(h[k]);
-                store_raw<BF16>(vec_at<BF16>(a.h_out, row * a.ldho, i), n[k], r);
+                store_raw<BF16>(h_out + off[k], n[k], r);
                 if (BF16) widen<BF16>(r, h[k]);
             }
         }
@@ -293,27 +308,25 @@ norm_residual_kernel(const NormArgs a) {
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(h[k][e], h[k][e], s2);
-        float ss[1] = {s2.x + s2.y};
-        block_sum<1>(ss, part[turn]);
+        const float rstd = rstd_of(block_sum(s2.x + s2.y, part[turn], tid, warps), (float)cols, a.eps);
         turn ^= 1;
-        const float rstd = rstd_of(ss[0], (float)cols, a.eps);
-        if (threadIdx.x == 0) a.rstd_pre[row] = rstd;
+        if (tid == 0) a.rstd_pre[row] = rstd;
+        char* y_out = row_at<BF16>(a.y, row * a.ldy);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = (int)threadIdx.x + k * T;
             const bool live = n[k] > 0;
             // y = RN(RN(h' w) rstd): for bf16 the first product is exact
             float2 t[PAIRS], f[PAIRS];
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) f[e] = both(0.0f);
-            if (live) w_pre.get(i, f);
+            if (live) w_pre.get(tid + k * T, f);
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) t[e] = __fmul2_rn(h[k][e], f[e]);
             if (a.y && live) {
                 float2 y[PAIRS];
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) y[e] = __fmul2_rn(t[e], both(rstd));
-                store_raw<BF16>(vec_at<BF16>(a.y, row * a.ldy, i), n[k], narrow<BF16>(y));
+                store_raw<BF16>(y_out + off[k], n[k], narrow<BF16>(y));
             }
             if (a.codes) {
                 // a block of 128 columns is 16 lanes' vectors; its codes follow from
@@ -325,7 +338,8 @@ norm_residual_kernel(const NormArgs a) {
                 for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
                 const Fp8Block b = fp8_block(m, rstd);
                 if (live) {
-                    if ((threadIdx.x & 15) == 0) a.scales[(int64_t)(i >> 4) * a.lp + row] = b.s;
+                    const int i = tid + k * T;
+                    if ((tid & 15) == 0) a.scales[(int64_t)(i >> 4) * a.lp + row] = b.s;
                     const uint2 q = make_uint2(fp8_codes4(t[0], t[1], b), fp8_codes4(t[2], t[3], b));
                     uint8_t* dst = a.codes + row * a.ldc + VEC * i;
                     if (n[k] >= VEC) {
@@ -349,45 +363,55 @@ norm_residual_kernel(const NormArgs a) {
 // dw_pre and dw_post run over all of a CTA's items.  Partial sums go to the
 // workspace and are added in a fixed order by norm_reduce_kernel, so results do
 // not depend on timing.
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 2 : 1)
+// FULL as above.  PARTS: which parts of the operator are there, or -1 to ask the
+// arguments.
+constexpr int PART_PRE = 1, PART_RES = 2, PART_POST = 4;
+template <bool BF16, int VPT, int THREADS, bool FULL, int PARTS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 2)
 norm_residual_backward_kernel(const NormBwdArgs a) {
+    constexpr uint32_t BYTES = VEC * (BF16 ? 2 : 4);
+    const bool pre = PARTS < 0 ? a.w_pre != nullptr : (PARTS & PART_PRE) != 0;
+    const bool res = PARTS < 0 ? a.o != nullptr : (PARTS & PART_RES) != 0;
+    const bool has_post = PARTS < 0 ? a.w_post != nullptr : (PARTS & PART_POST) != 0;
     extern __shared__ float4 columns[];
-    __shared__ float part[2][3][32];
-    const int T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT;
+    __shared__ float4 part[2][32];
+    const int tid = (int)threadIdx.x, T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT, warps = T >> 5;
     const Columns w_pre{columns, vecs}, factor{columns + 2 * vecs, vecs}, post{columns + 4 * vecs, vecs};
     const float inv_cols = 1.0f / (float)cols;
-    int n[VPT];
+    int n[VPT];                               // elements of this thread's vectors inside the row
+    uint32_t off[VPT];                        // and where they start
     float2 acc_pre[VPT][PAIRS];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int i = (int)threadIdx.x + k * T;
-        n[k] = cols - VEC * i;
+        const int i = tid + k * T;
+        n[k] = FULL ? VEC : cols - VEC * i;
+        off[k] = BYTES * (uint32_t)i;
         float2 v[PAIRS];
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) acc_pre[k][e] = v[e] = both(0.0f);
         post.set(i, v);
-        if (a.w_pre && n[k] > 0) {
-            widen<BF16>(load_raw<BF16>(vec_at<BF16>(a.w_pre, 0, i), n[k]), v);
+        if (pre && n[k] > 0) {
+            widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), v);
             w_pre.set(i, v);
         }
     }
     Raw<BF16> r_dhin[VPT], r_dy[VPT], r_h[VPT], r_o[VPT];
     float rstd2n = 0.0f, rstd1n = 1.0f;
     auto fetch = [&](int64_t row) {
-        if (a.w_pre) rstd2n = a.rstd_pre[row];
-        if (a.w_post) rstd1n = a.rstd_post[row];
+        if (pre) rstd2n = a.rstd_pre[row];
+        if (has_post) rstd1n = a.rstd_post[row];
+        const char* dhin = row_at<BF16>(a.dh_in, row * a.lddhi);
+        const char* dy = row_at<BF16>(a.dy, row * a.lddy);
+        const char* h = row_at<BF16>(a.h, row * a.ldh);
+        const char* o = row_at<BF16>(a.o, row * a.ldo);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = (int)threadIdx.x + k * T;
-            r_dhin[k] = r_dy[k] = r_h[k] = r_o[k] = zero_raw<BF16>();
-            if (n[k] <= 0) continue;
-            if (a.dh_in) r_dhin[k] = load_raw<BF16>(vec_at<BF16>(a.dh_in, row * a.lddhi, i), n[k]);
-            if (a.w_pre) {
-                r_dy[k] = load_raw<BF16>(vec_at<BF16>(a.dy, row * a.lddy, i), n[k]);
-                r_h[k] = load_raw<BF16>(vec_at<BF16>(a.h, row * a.ldh, i), n[k]);
+            r_dhin[k] = a.dh_in && n[k] > 0 ? load_raw<BF16>(dhin + off[k], n[k]) : zero_raw<BF16>();
+            if (pre) {
+                r_dy[k] = n[k] > 0 ? load_raw<BF16>(dy + off[k], n[k]) : zero_raw<BF16>();
+                r_h[k] = n[k] > 0 ? load_raw<BF16>(h + off[k], n[k]) : zero_raw<BF16>();
             }
-            if (a.o) r_o[k] = load_raw<BF16>(vec_at<BF16>(a.o, row * a.ldo, i), n[k]);
+            if (res) r_o[k] = n[k] > 0 ? load_raw<BF16>(o + off[k], n[k]) : zero_raw<BF16>();
         }
     };
     // the rows of item `it`
@@ -409,13 +433,12 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
         float2 acc[VPT][PAIRS];                    // sum dh' n1
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = (int)threadIdx.x + k * T;
             float2 f[PAIRS];
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) acc[k][e] = both(0.0f);
-            if (n[k] <= 0 || !a.o) continue;
-            branch_factor<BF16>(a.w_post, a.gate, a.ldg, a.alpha, grp, i, n[k], f);
-            factor.set(i, f);
+            if (n[k] <= 0 || !res) continue;
+            branch_factor<BF16>(has_post ? a.w_post : nullptr, a.gate, a.ldg, a.alpha, grp, off[k], n[k], f);
+            factor.set(tid + k * T, f);
         }
         for (; row < last; ++row) {
             const float rstd2 = rstd2n, rstd1 = rstd1n;
@@ -426,12 +449,14 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
             float2 s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int i = (int)threadIdx.x + k * T;
+                const int i = tid + k * T;
                 widen<BF16>(r_dhin[k], A[k]);
-                widen<BF16>(r_h[k], n2[k]);
-                widen<BF16>(r_o[k], n1[k]);
-                if (a.w_pre && n[k] > 0) {
+                if (res) widen<BF16>(r_o[k], n1[k]);
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) n2[k][e] = both(0.0f);
+                if (pre && n[k] > 0) {
                     float2 dy[PAIRS], w[PAIRS];
+                    widen<BF16>(r_h[k], n2[k]);
                     widen<BF16>(r_dy[k], dy);
                     w_pre.get(i, w);
 #pragma unroll
@@ -443,7 +468,7 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
                         A[k][e] = __ffma2_rn(d, both(rstd2), A[k][e]);
                     }
                 }
-                if (a.w_post && n[k] > 0) {
+                if (has_post && n[k] > 0) {
                     float2 f[PAIRS];
                     factor.get(i, f);
 #pragma unroll
@@ -458,48 +483,51 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
             if (row + 1 < last) fetch(row + 1);
             else if (row_next < last_next) fetch(row_next);
             float c1 = 0.0f, c2 = 0.0f;
-            if (a.w_pre || a.w_post) {
-                float sums[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
-                block_sum<3>(sums, part[turn]);
+            if (pre || has_post) {
+                const float4 sums = block_sum(make_float4(s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, 0.0f), part[turn], tid,
+                                              warps);
                 turn ^= 1;
-                c1 = rstd2 * (sums[0] * inv_cols);
-                c2 = (sums[1] - c1 * sums[2]) * inv_cols;
+                c1 = rstd2 * (sums.x * inv_cols);
+                c2 = (sums.y - c1 * sums.z) * inv_cols;
             }
+            char* dh_out = row_at<BF16>(a.dh, row * a.lddh);
+            char* do_out = row_at<BF16>(a.d_o, row * a.lddo);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int i = (int)threadIdx.x + k * T;
                 if (n[k] <= 0) continue;
+                if (pre) {
 #pragma unroll
-                for (int e = 0; e < PAIRS; ++e) A[k][e] = __ffma2_rn(n2[k][e], both(-c1), A[k][e]);      // dh'
-                store_raw<BF16>(vec_at<BF16>(a.dh, row * a.lddh, i), n[k], narrow<BF16>(A[k]));
-                if (!a.o) continue;
+                    for (int e = 0; e < PAIRS; ++e) A[k][e] = __ffma2_rn(n2[k][e], both(-c1), A[k][e]);      // dh'
+                }
+                store_raw<BF16>(dh_out + off[k], n[k], narrow<BF16>(A[k]));
+                if (!res) continue;
                 float2 f[PAIRS];
-                factor.get(i, f);
+                factor.get(tid + k * T, f);
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
                     acc[k][e] = __ffma2_rn(A[k][e], n1[k][e], acc[k][e]);
                     f[e] = __fmul2_rn(A[k][e], f[e]);                                    // b, or do itself
-                    if (a.w_post) f[e] = __fmul2_rn(__ffma2_rn(n1[k][e], both(-c2), f[e]), both(rstd1));
+                    if (has_post) f[e] = __fmul2_rn(__ffma2_rn(n1[k][e], both(-c2), f[e]), both(rstd1));
                 }
-                store_raw<BF16>(vec_at<BF16>(a.d_o, row * a.lddo, i), n[k], narrow<BF16>(f));
+                store_raw<BF16>(do_out + off[k], n[k], narrow<BF16>(f));
             }
         }
-        if (a.gate || a.w_post) {
+        if (a.gate || has_post) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int i = (int)threadIdx.x + k * T;
+                const int i = tid + k * T;
                 if (n[k] <= 0) continue;
                 float2 f[PAIRS];
-                if (a.w_post) {
+                if (has_post) {
                     float2 p[PAIRS];
-                    branch_factor<BF16>(nullptr, a.gate, a.ldg, a.alpha, grp, i, n[k], f);
+                    branch_factor<BF16>(nullptr, a.gate, a.ldg, a.alpha, grp, off[k], n[k], f);
                     post.get(i, p);
 #pragma unroll
                     for (int e = 0; e < PAIRS; ++e) p[e] = __ffma2_rn(f[e], acc[k][e], p[e]);
                     post.set(i, p);
                 }
                 if (a.gate) {
-                    branch_factor<BF16>(a.w_post, nullptr, 0, a.alpha, 0, i, n[k], f);
+                    branch_factor<BF16>(has_post ? a.w_post : nullptr, nullptr, 0, a.alpha, 0, off[k], n[k], f);
 #pragma unroll
                     for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], acc[k][e]);
                     float* dst = a.gate_part + item * a.gate_pitch + VEC * i;
@@ -519,11 +547,11 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int i = (int)threadIdx.x + k * T;
+        const int i = tid + k * T;
         if (n[k] <= 0) continue;
         const int64_t at = (int64_t)blockIdx.x * a.pitch + VEC * i;
-        if (a.w_pre) store_raw<false>(a.pre_part + at, n[k], narrow<false>(acc_pre[k]));
-        if (a.w_post) {
+        if (pre) store_raw<false>(a.pre_part + at, n[k], narrow<false>(acc_pre[k]));
+        if (has_post) {
             float2 p[PAIRS];
             post.get(i, p);
             store_raw<false>(a.post_part + at, n[k], narrow<false>(p));
@@ -534,8 +562,8 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
 // out[g][c] = sum over p < n of part[g * n + p][c], in a fixed order; the jobs
 // dw_pre, dw_post and dgate (one per group) along the grid's y
 __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormBwdArgs a, int ctas) {
-    __shared__ float s[8][33];
-    int job = (int)blockIdx.y;
+    __shared__ float4 sums[32][9];
+    const int job = (int)blockIdx.y, quad = (int)threadIdx.x & 7, y = (int)threadIdx.x >> 3;
     const float* part;
     float* out;
     int64_t n = ctas;
@@ -551,39 +579,52 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormBwdArgs a, i
         part = a.gate_part + g * n * a.pitch;
         out = a.dgate + g * a.cols;
     }
-    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-    const int y = threadIdx.x >> 5;
-    float v = 0.0f;
-    if (c < a.cols)
-        for (int64_t p = y; p < n; p += 8) v += part[p * a.pitch + c];
-    s[y][threadIdx.x & 31] = v;
+    // 32 columns, four per thread; every 32nd line per thread, then over the threads
+    const int64_t c = (int64_t)blockIdx.x * 32 + 4 * quad;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < a.cols) {
+#pragma unroll 4
+        for (int64_t p = y; p < n; p += 32) {
+            const float4 w = *reinterpret_cast<const float4*>(part + p * a.pitch + c);
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
+        }
+    }
+    sums[y][quad] = v;
     __syncthreads();
-    if (y == 0 && c < a.cols) {
-        for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
-        out[c] = v;
+    if (threadIdx.x < 32) {
+        const int col = (int)threadIdx.x;
+        const float* s = reinterpret_cast<const float*>(&sums[0][0]) + col;
+        float t = s[0];
+        for (int i = 1; i < 32; ++i) t += s[i * 36];
+        if ((int64_t)blockIdx.x * 32 + col < a.cols) out[(int64_t)blockIdx.x * 32 + col] = t;
     }
 }
 
-// vectors per thread and threads for a row of `cols` elements
+// vectors per thread and threads for a row of `cols` elements.  Two vectors per
+// thread up to 4096 columns leave registers for three CTAs of 256 threads per SM:
+// norm 8192 x 4096 52.9 us, against 67.6 with one vector and 512 threads, 58.9
+// with two CTAs per SM and 66.4 with four, which spill.
 void shape_of(int64_t cols, int& vpt, int& threads) {
     const int64_t nvec = (cols + VEC - 1) / VEC;
     vpt = nvec <= 256 ? 1 : (nvec <= 1024 ? 2 : 4);
     threads = (int)(((nvec + vpt - 1) / vpt + 31) / 32 * 32);
 }
 
-template <bool BF16, int VPT, bool RES, bool POST>
+template <bool BF16, int VPT, int THREADS, bool FULL, bool RES, bool POST>
 cudaError_t run_norm(const NormArgs& a, int threads, cudaStream_t s) {
     static PerDeviceOnce setup;
     static int per_sm[kOnceDevices][17] = {};
+    constexpr auto kernel = norm_residual_kernel<BF16, VPT, THREADS, FULL, RES, POST>;
     const auto smem = [](int t) { return (size_t)t * VPT * VEC * sizeof(float) * (RES ? 2 : 1); };
     int dev = 0;
     const cudaError_t e = setup.run([&](int d) {
-        cudaError_t err = cudaFuncSetAttribute(norm_residual_kernel<BF16, VPT, RES, POST>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(512));
-        for (int w = 1; w <= (VPT == 1 ? 8 : 16) && err == cudaSuccess; ++w) {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(THREADS));
+        for (int w = 1; w <= THREADS / 32 && err == cudaSuccess; ++w) {
             int n = 0;
-            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_residual_kernel<BF16, VPT, RES, POST>, 32 * w,
-                                                                smem(32 * w));
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 32 * w, smem(32 * w));
             per_sm[d][w] = n < 1 ? 1 : n;
         }
         return err;
@@ -591,33 +632,63 @@ cudaError_t run_norm(const NormArgs& a, int threads, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t cap = (int64_t)num_sms() * per_sm[dev][threads / 32];
     const unsigned grid = (unsigned)(a.rows < cap ? a.rows : cap);
-    norm_residual_kernel<BF16, VPT, RES, POST><<<grid, threads, smem(threads), s>>>(a);
+    kernel<<<grid, threads, smem(threads), s>>>(a);
     return cudaGetLastError();
 }
 
-template <bool BF16, int VPT>
+template <bool BF16, int VPT, int THREADS, bool FULL>
 cudaError_t run_norm_parts(const NormArgs& a, int threads, cudaStream_t s) {
-    if (!a.o) return run_norm<BF16, VPT, false, false>(a, threads, s);
-    return a.w_post ? run_norm<BF16, VPT, true, true>(a, threads, s) : run_norm<BF16, VPT, true, false>(a, threads, s);
+    if (!a.o) return run_norm<BF16, VPT, THREADS, FULL, false, false>(a, threads, s);
+    return a.w_post ? run_norm<BF16, VPT, THREADS, FULL, true, true>(a, threads, s)
+                    : run_norm<BF16, VPT, THREADS, FULL, true, false>(a, threads, s);
 }
 
-template <bool BF16, int VPT>
+template <bool BF16, int VPT, int THREADS, bool FULL, int PARTS>
 cudaError_t run_norm_bwd(const NormBwdArgs& a, int threads, cudaStream_t s) {
     static PerDeviceOnce setup;
+    constexpr auto kernel = norm_residual_backward_kernel<BF16, VPT, THREADS, FULL, PARTS>;
     const auto smem = [](int t) { return (size_t)t * VPT * VEC * sizeof(float) * 3; };
     cudaError_t e = setup.run([&](int) {
-        return cudaFuncSetAttribute(norm_residual_backward_kernel<BF16, VPT>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(512));
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(THREADS));
     });
     if (e != cudaSuccess) return e;
     const int ctas = (int)(a.items < NORM_BWD_CTAS ? a.items : NORM_BWD_CTAS);
-    norm_residual_backward_kernel<BF16, VPT><<<ctas, threads, smem(threads), s>>>(a);
+    kernel<<<ctas, threads, smem(threads), s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t jobs = (a.w_pre ? 1 : 0) + (a.w_post ? 1 : 0) + ((a.gate && a.nseg > 1) ? a.groups : 0);
     if (jobs == 0) return cudaSuccess;
     norm_reduce_kernel<<<dim3((unsigned)((a.cols + 31) / 32), (unsigned)jobs), 256, 0, s>>>(a, ctas);
     return cudaGetLastError();
+}
+
+template <bool BF16, int VPT, int THREADS, bool FULL>
+cudaError_t run_norm_bwd_parts(const NormBwdArgs& a, int threads, cudaStream_t s) {
+    // the usual blocks compiled for themselves where rows are whole
+    if (FULL && a.w_pre && a.o && a.w_post)
+        return run_norm_bwd<BF16, VPT, THREADS, FULL, FULL ? PART_PRE | PART_RES | PART_POST : -1>(a, threads, s);
+    if (FULL && a.w_pre && a.o) return run_norm_bwd<BF16, VPT, THREADS, FULL, FULL ? PART_PRE | PART_RES : -1>(a, threads, s);
+    return run_norm_bwd<BF16, VPT, THREADS, FULL, -1>(a, threads, s);
+}
+
+template <bool BF16, int VPT, int THREADS>
+cudaError_t launch_shape(const NormArgs& a, int threads, cudaStream_t s) {
+    return a.cols == (int64_t)threads * VPT * VEC ? run_norm_parts<BF16, VPT, THREADS, true>(a, threads, s)
+                                                  : run_norm_parts<BF16, VPT, THREADS, false>(a, threads, s);
+}
+template <bool BF16, int VPT, int THREADS>
+cudaError_t launch_shape(const NormBwdArgs& a, int threads, cudaStream_t s) {
+    return a.cols == (int64_t)threads * VPT * VEC ? run_norm_bwd_parts<BF16, VPT, THREADS, true>(a, threads, s)
+                                                  : run_norm_bwd_parts<BF16, VPT, THREADS, false>(a, threads, s);
+}
+
+template <bool BF16, class Args>
+cudaError_t launch_columns(const Args& a, cudaStream_t s) {
+    int vpt, threads;
+    shape_of(a.cols, vpt, threads);
+    if (vpt == 1) return launch_shape<BF16, 1, 256>(a, threads, s);
+    if (vpt == 4) return launch_shape<BF16, 4, 512>(a, threads, s);
+    return threads <= 256 ? launch_shape<BF16, 2, 256>(a, threads, s) : launch_shape<BF16, 2, 512>(a, threads, s);
 }
 
 }  // namespace
@@ -641,13 +712,7 @@ size_t norm_bwd_workspace(const NormBwdArgs& a) {
 }
 
 cudaError_t launch_norm(const NormArgs& a, bool bf16, cudaStream_t s) {
-    int vpt, threads;
-    shape_of(a.cols, vpt, threads);
-    switch (vpt) {
-    case 1: return bf16 ? run_norm_parts<true, 1>(a, threads, s) : run_norm_parts<false, 1>(a, threads, s);
-    case 2: return bf16 ? run_norm_parts<true, 2>(a, threads, s) : run_norm_parts<false, 2>(a, threads, s);
-    default: return bf16 ? run_norm_parts<true, 4>(a, threads, s) : run_norm_parts<false, 4>(a, threads, s);
-    }
+    return bf16 ? launch_columns<true>(a, s) : launch_columns<false>(a, s);
 }
 
 cudaError_t launch_norm_bwd(NormBwdArgs a, bool bf16, float* workspace, cudaStream_t s) {
@@ -657,13 +722,7 @@ cudaError_t launch_norm_bwd(NormBwdArgs a, bool bf16, float* workspace, cudaStre
     // one item per group: its sums are dgate's row
     a.gate_part = a.nseg > 1 ? a.post_part + (a.w_post ? ctas * a.pitch : 0) : a.dgate;
     a.gate_pitch = a.nseg > 1 ? a.pitch : a.cols;
-    int vpt, threads;
-    shape_of(a.cols, vpt, threads);
-    switch (vpt) {
-    case 1: return bf16 ? run_norm_bwd<true, 1>(a, threads, s) : run_norm_bwd<false, 1>(a, threads, s);
-    case 2: return bf16 ? run_norm_bwd<true, 2>(a, threads, s) : run_norm_bwd<false, 2>(a, threads, s);
-    default: return bf16 ? run_norm_bwd<true, 4>(a, threads, s) : run_norm_bwd<false, 4>(a, threads, s);
-    }
+    return bf16 ? launch_columns<true>(a, s) : launch_columns<false>(a, s);
 }
 
 }  // namespace fp4
