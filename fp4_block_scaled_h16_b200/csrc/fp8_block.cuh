@@ -4,15 +4,12 @@
 // With m the block's largest magnitude the scale is s = RN(m / 448) (1 where that
 // is below the smallest normal binary32) and the code of x is E4M3_rne(448 x / m).
 // bf16 values, and products of two of them, often lie exactly in the middle of
-// two codes, where a quotient that is off by one ulp takes the wrong one.  So the
-// quotient is a product with the rounded 448 / m, corrected once by its remainder
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990):
-//   v0 = RN(x c), c = RN(448 / m);   e = v0 (m / 512) - 7/8 x;   v = v0 - e r,
-//   r = RN(512 / m)
-// which is exact wherever binary32 holds the quotient and 7 x, and keeps the
-// sign of a zero (e is +0 there).  Four packed operations for two elements,
-// instead of two divisions.
+// two codes, where a quotient that is off by one ulp takes the wrong one.  So
+// 448 / m is held as an unevaluated sum of two binary32, c + d, with c a little
+// below it and d >= 0 the rest (Dekker, "A floating-point technique for extending
+// the available precision", 1971), within 2^-40 of it, and the quotient is
+// RN(x c + RN(x d)): exact wherever binary32 holds it, and with the sign of a
+// zero kept.  Two packed operations for two elements, instead of two divisions.
 #pragma once
 
 #include <cstdint>
@@ -22,32 +19,37 @@ namespace fp4 {
 
 struct Fp8Block {
     float s;        // the stored scale
-    float c;        // 448 / m
-    float m;        // m / 512
-    float nr;       // -512 / m
+    float c, d;     // 448 / m
 };
+
+// RN(x / 448): a product with RN(1 / 448) corrected by its remainder (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990), where that remainder does not underflow
+__device__ __forceinline__ float over_448(float x) {
+    if (x < 0x1p-90f) return __fdiv_rn(x, 448.0f);
+    const float q = __fmul_rn(x, 1.0f / 448.0f);
+    return __fmaf_rn(__fmaf_rn(-448.0f, q, x), 1.0f / 448.0f, q);
+}
 
 // m the largest |x|, and `times` what the values still have to be multiplied by
 __device__ __forceinline__ Fp8Block fp8_block(float m, float times = 1.0f) {
     Fp8Block b;
-    b.s = __fdiv_rn(__fmul_rn(m, times), 448.0f);
+    b.s = over_448(__fmul_rn(m, times));
     if (b.s >= 1.17549435e-38f) {
-        b.c = __fdiv_rn(448.0f, m);
-        b.m = __fmul_rn(m, 0x1p-9f);
-        b.nr = -__frcp_rn(b.m);
+        float r;                                            // 1 / m within 2^-22
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(m));
+        b.c = __fmul_rn(448.0f * (1.0f - 0x1p-20f), r);     // below 448 / m by 2^-21 to 2^-19 of it
+        b.d = __fmul_rn(__fmaf_rn(-b.c, m, 448.0f), r);
     } else {        // an all but zero block: codes of the values themselves
         b.s = 1.0f;
         b.c = times;
-        b.m = 0.0f;
-        b.nr = -0.0f;
+        b.d = 0.0f;
     }
     return b;
 }
 
 __device__ __forceinline__ float2 fp8_quotient(float2 x, const Fp8Block& b) {
-    const float2 v = __fmul2_rn(x, make_float2(b.c, b.c));
-    const float2 e = __ffma2_rn(v, make_float2(b.m, b.m), __fmul2_rn(x, make_float2(-0.875f, -0.875f)));
-    return __ffma2_rn(e, make_float2(b.nr, b.nr), v);
+    return __ffma2_rn(x, make_float2(b.c, b.c), __fmul2_rn(x, make_float2(b.d, b.d)));
 }
 
 // the codes of four elements, the first in the low byte; the conversion saturates to 448

@@ -481,8 +481,8 @@ size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines);
  * largest |x| of a block:
  *     s = RN(m / 448)  (1 where that is below the smallest normal binary32),
  *     code = E4M3_rne_satfinite(448 x / m)  (of x itself where s is 1 for that),
- * the quotient taken in binary32: exactly rounded for bf16 inputs, within two
- * units in the last place for fp32 inputs.
+ * the quotient rounded to binary32 first (for fp32 inputs within 2^-16 of a unit
+ * in the last place of the exactly rounded one).
  *   x, in_dtype, rows, cols, ld   input, as fp4_quantize; any rows and cols
  *   block_lines     1 or 128
  *   codes_rows, ld_rows, scales_rows   the rows' result, or codes_rows NULL
