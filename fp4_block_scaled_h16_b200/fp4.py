@@ -104,7 +104,7 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -440,30 +440,49 @@ def fp4_fp8_block_gemm(a_codes, lda, a_scales, b_codes, ldb, b_scales, b_block_l
            "fp4_fp8_block_gemm")
 
 
-def _pitch(t) -> int:
-    """Row pitch in elements of a 2-D tensor with unit stride in its last dim."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+# The helpers below look at every tensor before its address is handed on.  A call
+# for one token takes a few microseconds on the GPU, so the checks read each
+# property once and build their messages only when they fail.
 
-
-def _want(t, what: str, shape=None, dtype=None, like=None):
-    """Refuse a tensor that the call would read or write wrongly."""
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (what, shape, tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.numel() and t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("%s must have unit stride in its last dimension" % what)
-    if like is not None and t.device != like.device:
-        raise ValueError("%s is on %s, the other tensors on %s" % (what, t.device, like.device))
-
-
-def _on_current_device(t, what: str):
-    """The library launches on the current device; a tensor of another one is refused."""
+def _device_of(t, what: str) -> int:
+    """The device index of a CUDA tensor; the library launches on the current
+    device, so a tensor of another one is refused."""
     import torch
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("%s must be a CUDA tensor" % what)
-    if t.get_device() != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
+    return dev
+
+
+def _mat(t, what: str, shape, dtype, dev) -> int:
+    """Row pitch in elements of a [rows, cols] tensor with unit stride in its
+    last dimension, of this type and on this device."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the other tensors on device %d" % (what, t.device, dev))
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError("%s must have unit stride in its last dimension" % what)
+    # the pitch of a single row is not used, and torch may call it anything
+    return ld if shape[0] > 1 else (shape[1] + 15) // 16 * 16
+
+
+def _flat(t, what: str, shape, dtype, dev):
+    """A contiguous tensor of this shape and type on this device."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the other tensors on device %d" % (what, t.device, dev))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t
 
 
 def alloc_fp8_block(lines: int, K: int, block_lines: int = 1, device="cuda"):
@@ -477,27 +496,39 @@ def alloc_fp8_block(lines: int, K: int, block_lines: int = 1, device="cuda"):
                 lines=lines, K=K, block_lines=block_lines)
 
 
-def _fp8_tensor(q, what: str, lines: int, K: int, block_lines: int, like):
-    """Codes, their pitch and the scales of an FP8 tensor, checked."""
+def _fp8_tensor(q, what: str, lines: int, K: int, block_lines: int, dev):
+    """Address and pitch of the codes and address of the scales of an FP8 tensor, checked."""
     import torch
     codes, scales = q["codes"], q["scales"]
-    if q["lines"] != lines or q["K"] != K or q["block_lines"] != block_lines:
+    if q["lines"] != lines or q["K"] != K or q["block_lines"] != block_lines or block_lines not in (1, 128):
         raise ValueError("%s must hold %d lines of %d in blocks of %d lines" % (what, lines, K, block_lines))
-    if codes.dim() != 2 or codes.shape[0] != lines or codes.shape[1] < K:
+    width = codes.shape[-1]
+    if width < K:
         raise ValueError("%s: codes must be [%d, >= %d], got %s" % (what, lines, K, tuple(codes.shape)))
-    _want(codes, what + " codes", dtype=torch.uint8, like=like)
+    ld = _mat(codes, what + " codes", (lines, width), torch.uint8, dev)
     n = (lines + 127) // 128 * (128 if block_lines == 1 else 1)
-    _want(scales, what + " scales", shape=((K + 127) // 128, n), dtype=torch.float32, like=like)
-    if not scales.is_contiguous():
-        raise ValueError("%s: scales must be contiguous" % what)
-    return codes, _pitch(codes), scales
+    _flat(scales, what + " scales", ((K + 127) // 128, n), torch.float32, dev)
+    return codes.data_ptr(), ld, scales.data_ptr()
 
 
-def _fp8_quantize(x, block_lines, rows_q, cols_q, stream):
-    rows, cols = x.shape
-    cr = _fp8_tensor(rows_q, "the rows' result", rows, cols, block_lines, x) if rows_q is not None else (None, 0, None)
-    cc = _fp8_tensor(cols_q, "the columns' result", cols, rows, block_lines, x) if cols_q is not None else (None, 0, None)
-    fp4_fp8_block_quantize(x, in_dtype_of(x), rows, cols, _pitch(x), block_lines, *cr, *cc, stream)
+_NO_FP8 = (None, 0, None)
+
+
+def _fp8_quantize(x, block_lines, out_rows, out_cols, want_rows, want_cols, stream):
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D, got %s" % (tuple(x.shape),))
+    shape = rows, cols = x.shape
+    dt, ld = in_dtype_of(x), _mat(x, "x", shape, x.dtype, dev)
+    if want_rows and out_rows is None:
+        out_rows = alloc_fp8_block(rows, cols, block_lines, x.device)
+    if want_cols and out_cols is None:
+        out_cols = alloc_fp8_block(cols, rows, block_lines, x.device)
+    r = _fp8_tensor(out_rows, "the rows' result", rows, cols, block_lines, dev) if want_rows else _NO_FP8
+    c = _fp8_tensor(out_cols, "the columns' result", cols, rows, block_lines, dev) if want_cols else _NO_FP8
+    _check(_lib.fp4_fp8_block_quantize(x.data_ptr(), dt, rows, cols, ld, block_lines, *r, *c, _stream(stream)),
+           "fp4_fp8_block_quantize")
+    return out_rows, out_cols
 
 
 def fp8_block_quantize(x, axis=1, block_lines=1, out=None, stream=None):
@@ -505,26 +536,17 @@ def fp8_block_quantize(x, axis=1, block_lines=1, out=None, stream=None):
     (axis 1) or its columns (axis 0: the transposed tensor), of block_lines (1
     or 128) lines (fp4_fp8_block_quantize); into a new or given FP8 tensor
     {"codes", "scales", "lines", "K", "block_lines"}."""
-    if axis not in (0, 1):
-        raise ValueError("axis must be 0 or 1, got %r" % (axis,))
-    _on_current_device(x, "x")
-    _want(x, "x")
-    rows, cols = x.shape
-    q = out if out is not None else alloc_fp8_block(*((rows, cols) if axis else (cols, rows)), block_lines, x.device)
-    _fp8_quantize(x, block_lines, q if axis else None, None if axis else q, stream)
-    return q
+    if axis == 1:
+        return _fp8_quantize(x, block_lines, out, None, True, False, stream)[0]
+    if axis == 0:
+        return _fp8_quantize(x, block_lines, None, out, False, True, stream)[1]
+    raise ValueError("axis must be 0 or 1, got %r" % (axis,))
 
 
 def fp8_block_quantize_both_axes(x, block_lines=1, out_rows=None, out_cols=None, stream=None):
     """fp8_block_quantize along the rows and along the columns from one read;
     returns (FP8 tensor of the rows, FP8 tensor of the columns)."""
-    _on_current_device(x, "x")
-    _want(x, "x")
-    rows, cols = x.shape
-    qr = out_rows if out_rows is not None else alloc_fp8_block(rows, cols, block_lines, x.device)
-    qc = out_cols if out_cols is not None else alloc_fp8_block(cols, rows, block_lines, x.device)
-    _fp8_quantize(x, block_lines, qr, qc, stream)
-    return qr, qc
+    return _fp8_quantize(x, block_lines, out_rows, out_cols, True, True, stream)
 
 
 def fp8_block_gemm(qa, qb, out_dtype=FP4_OUT_F32, out=None, stream=None):
@@ -534,15 +556,15 @@ def fp8_block_gemm(qa, qb, out_dtype=FP4_OUT_F32, out=None, stream=None):
     M, N, K = qa["lines"], qb["lines"], qa["K"]
     if qb["K"] != K or qa["block_lines"] != 1:
         raise ValueError("operands must share K, and A must have 1 x 128 blocks")
-    _on_current_device(qa["codes"], "A")
-    a, lda, sa = _fp8_tensor(qa, "A", M, K, 1, qa["codes"])
-    b, ldb, sb = _fp8_tensor(qb, "B", N, K, qb["block_lines"], a)
+    dev = _device_of(qa["codes"], "A")
+    a = _fp8_tensor(qa, "A", M, K, 1, dev)
+    b = _fp8_tensor(qb, "B", N, K, qb["block_lines"], dev)
     dtype = torch.bfloat16 if out_dtype == FP4_OUT_BF16 else torch.float32
     if out is None:
-        out = torch.empty((M, (N + 7) // 8 * 8), dtype=dtype, device=a.device)[:, :N]
-    else:
-        _want(out, "out", shape=(M, N), dtype=dtype, like=a)
-    fp4_fp8_block_gemm(a, lda, sa, b, ldb, sb, qb["block_lines"], M, N, K, out, out_dtype, _pitch(out), stream)
+        out = torch.empty((M, (N + 7) // 8 * 8), dtype=dtype, device=qa["codes"].device)[:, :N]
+    ldc = _mat(out, "out", (M, N), dtype, dev)
+    _check(_lib.fp4_fp8_block_gemm(*a, *b, qb["block_lines"], M, N, K, out.data_ptr(), out_dtype, ldc, _stream(stream)),
+           "fp4_fp8_block_gemm")
     return out
 
 
@@ -574,37 +596,40 @@ def fp4_norm_residual_backward(dy, lddy, dh_in, ld_dhin, h, ldh, o, ldo, dtype, 
                                            workspace_bytes, _stream(stream)), "fp4_norm_residual_backward")
 
 
-def _mat(t, what, shape, like):
-    """(tensor, row pitch) of an optional [rows, cols] tensor of like's type."""
-    if t is None:
-        return None, 0
-    _want(t, what, shape=shape, dtype=like.dtype, like=like)
-    return t, _pitch(t)
+def _opt_mat(t, what: str, shape, dtype, dev):
+    """(address, row pitch) of an optional [rows, cols] tensor."""
+    return (None, 0) if t is None else (t.data_ptr(), _mat(t, what, shape, dtype, dev))
 
 
-def _gate_of(gate, rows_per_group, rows, cols, like):
+def _opt_flat(t, what: str, shape, dtype, dev):
+    """Address of an optional contiguous tensor."""
+    return None if t is None else _flat(t, what, shape, dtype, dev).data_ptr()
+
+
+def _gate_of(gate, rows_per_group, rows, cols, dtype, dev):
+    """(address, row pitch, rows per group) of an optional gate."""
     if gate is None:
         return None, 0, 0
     if rows_per_group is None or rows_per_group < 1:
         raise ValueError("a gate needs rows_per_group >= 1")
-    t, ld = _mat(gate, "gate", ((rows + rows_per_group - 1) // rows_per_group, cols), like)
-    return t, ld, rows_per_group
+    shape = ((rows + rows_per_group - 1) // rows_per_group, cols)
+    return gate.data_ptr(), _mat(gate, "gate", shape, dtype, dev), rows_per_group
 
 
-def _float_vector(t, what, shape, like):
+def _new_vector(t, what: str, shape, like, dev):
+    """A given float32 buffer, checked, or a new one."""
     import torch
     if t is None:
         return torch.empty(shape, dtype=torch.float32, device=like.device)
-    _want(t, what, shape=shape, dtype=torch.float32, like=like)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t
+    return _flat(t, what, shape, torch.float32, dev)
 
 
-def _blank(like, rows, cols):
-    """A [rows, cols] tensor of like's type whose row pitch is a multiple of 16 bytes."""
+def _new_mat(t, like, shape):
+    """A given buffer, or a new [rows, cols] tensor of like's type whose row pitch is a multiple of 16 bytes."""
     import torch
-    return torch.empty((rows, (cols + 7) // 8 * 8), dtype=like.dtype, device=like.device)[:, :cols]
+    if t is not None:
+        return t
+    return torch.empty((shape[0], (shape[1] + 7) // 8 * 8), dtype=like.dtype, device=like.device)[:, :shape[1]]
 
 
 def norm_residual(h, w_pre=None, o=None, w_post=None, gate=None, rows_per_group=None, alpha=1.0, eps=1e-6,
@@ -615,36 +640,43 @@ def norm_residual(h, w_pre=None, o=None, w_post=None, gate=None, rows_per_group=
     h' (h itself without o), "rstd_post", "rstd_pre", and with w_pre "y", or
     with quantize=True "q", y as an FP8 tensor of 1 x 128 blocks}.  `out` may
     hold buffers under those names; out["y"] and out["q"] together get both."""
-    _on_current_device(h, "h")
-    _want(h, "h")
-    rows, cols = h.shape
-    out = out or {}
-    if o is None and w_pre is None:
-        raise ValueError("nothing to do: neither o nor w_pre is given")
-    if o is None and (w_post is not None or gate is not None):
-        raise ValueError("w_post and gate belong to a block output o")
-    o, ldo = _mat(o, "o", (rows, cols), h)
-    for w, what in ((w_pre, "w_pre"), (w_post, "w_post")):
-        if w is not None:
-            _want(w, what, shape=(cols,), dtype=h.dtype, like=h)
-    gate, ldg, per = _gate_of(gate, rows_per_group, rows, cols, h)
-    got, h_out, ld_hout = dict(h=h, rstd_post=None, rstd_pre=None), None, 0
+    dev = _device_of(h, "h")
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D, got %s" % (tuple(h.shape),))
+    shape = rows, cols = h.shape
+    dt, dtype, out = in_dtype_of(h), h.dtype, out or {}
+    ldh = _mat(h, "h", shape, dtype, dev)
+    if o is None:
+        if w_pre is None:
+            raise ValueError("nothing to do: neither o nor w_pre is given")
+        if w_post is not None or gate is not None:
+            raise ValueError("w_post and gate belong to a block output o")
+    got = dict(h=h, rstd_post=None, rstd_pre=None)
+    po = ph = (None, 0)
     if o is not None:
-        h_out, ld_hout = _mat(out["h"] if out.get("h") is not None else _blank(h, rows, cols), "out h", (rows, cols), h)
-        got["h"] = h_out
+        po = _opt_mat(o, "o", shape, dtype, dev)
+        got["h"] = _new_mat(out.get("h"), h, shape)
+        ph = _opt_mat(got["h"], "out h", shape, dtype, dev)
+    p_post = _opt_flat(w_post, "w_post", (cols,), dtype, dev)
+    p_pre = _opt_flat(w_pre, "w_pre", (cols,), dtype, dev)
+    gate = _gate_of(gate, rows_per_group, rows, cols, dtype, dev)
+    r_post = r_pre = None
     if w_post is not None:
-        got["rstd_post"] = _float_vector(out.get("rstd_post"), "rstd_post", (rows,), h)
-    y, ldy, q = None, 0, (None, 0, None)
+        got["rstd_post"] = _new_vector(out.get("rstd_post"), "rstd_post", (rows,), h, dev)
+        r_post = got["rstd_post"].data_ptr()
+    y, q = (None, 0), _NO_FP8
     if w_pre is not None:
-        got["rstd_pre"] = _float_vector(out.get("rstd_pre"), "rstd_pre", (rows,), h)
-        if quantize or out.get("q") is not None:
-            got["q"] = out["q"] if out.get("q") is not None else alloc_fp8_block(rows, cols, 1, h.device)
-            q = _fp8_tensor(got["q"], "q", rows, cols, 1, h)
-        if not quantize or out.get("y") is not None:
-            y, ldy = _mat(out["y"] if out.get("y") is not None else _blank(h, rows, cols), "y", (rows, cols), h)
-            got["y"] = y
-    fp4_norm_residual(o, ldo, h, _pitch(h), in_dtype_of(h), rows, cols, w_post, gate, ldg, per, alpha, w_pre, eps,
-                      h_out, ld_hout, y, ldy, *q, got["rstd_post"], got["rstd_pre"], stream)
+        got["rstd_pre"] = _new_vector(out.get("rstd_pre"), "rstd_pre", (rows,), h, dev)
+        r_pre = got["rstd_pre"].data_ptr()
+        given_y, given_q = out.get("y"), out.get("q")
+        if quantize or given_q is not None:
+            got["q"] = given_q if given_q is not None else alloc_fp8_block(rows, cols, 1, h.device)
+            q = _fp8_tensor(got["q"], "q", rows, cols, 1, dev)
+        if not quantize or given_y is not None:
+            got["y"] = _new_mat(given_y, h, shape)
+            y = _opt_mat(got["y"], "y", shape, dtype, dev)
+    _check(_lib.fp4_norm_residual(*po, h.data_ptr(), ldh, dt, rows, cols, p_post, *gate, alpha, p_pre, eps, *ph, *y, *q,
+                                  r_post, r_pre, _stream(stream)), "fp4_norm_residual")
     return got
 
 
@@ -659,47 +691,47 @@ def norm_residual_backward(dy, h, rstd_pre=None, w_pre=None, dh_in=None, o=None,
     like = dy if dy is not None else dh_in
     if like is None:
         raise ValueError("neither dy nor dh_in is given")
-    _on_current_device(like, "the incoming gradient")
-    rows, cols = like.shape
-    shape = (rows, cols)
-    out = out or {}
+    dev = _device_of(like, "the incoming gradient")
+    if like.dim() != 2:
+        raise ValueError("the incoming gradient must be 2-D, got %s" % (tuple(like.shape),))
+    shape = rows, cols = like.shape
+    dt, dtype, f32, out = in_dtype_of(like), like.dtype, torch.float32, out or {}
     if (dy is None) != (w_pre is None) or (w_pre is not None and (rstd_pre is None or h is None)):
         raise ValueError("dy, w_pre, rstd_pre and h go together")
     if o is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate belong to a block output o")
     if w_post is not None and rstd_post is None:
         raise ValueError("w_post and rstd_post go together")
-    dy, lddy = _mat(dy, "dy", shape, like)
-    dh_in, lddhi = _mat(dh_in, "dh_in", shape, like)
-    h, ldh = _mat(h, "h", shape, like) if w_pre is not None else (None, 0)
-    o, ldo = _mat(o, "o", shape, like)
-    for w, what in ((w_pre, "w_pre"), (w_post, "w_post")):
-        if w is not None:
-            _want(w, what, shape=(cols,), dtype=like.dtype, like=like)
-    for r, what, w in ((rstd_pre, "rstd_pre", w_pre), (rstd_post, "rstd_post", w_post)):
-        if w is not None:
-            _float_vector(r, what, (rows,), like)
-    gate, ldg, per = _gate_of(gate, rows_per_group, rows, cols, like)
-    pick = lambda name: out[name] if out.get(name) is not None else _blank(like, rows, cols)  # noqa: E731
-    got = dict(dh=pick("dh"), do=None, dw_pre=None, dw_post=None, dgate=None)
-    dh, lddh = _mat(got["dh"], "out dh", shape, like)
-    d_o, lddo = None, 0
+    has_pre, has_post, has_gate = w_pre is not None, w_post is not None, gate is not None
+    p_dy = _opt_mat(dy, "dy", shape, dtype, dev)
+    p_in = _opt_mat(dh_in, "dh_in", shape, dtype, dev)
+    p_h = _opt_mat(h if has_pre else None, "h", shape, dtype, dev)
+    p_o = _opt_mat(o, "o", shape, dtype, dev)
+    p_pre = _opt_flat(w_pre, "w_pre", (cols,), dtype, dev)
+    p_post = _opt_flat(w_post, "w_post", (cols,), dtype, dev)
+    r_pre = _opt_flat(rstd_pre if has_pre else None, "rstd_pre", (rows,), f32, dev)
+    r_post = _opt_flat(rstd_post if has_post else None, "rstd_post", (rows,), f32, dev)
+    gate_shape = gate.shape if has_gate else None
+    gate = _gate_of(gate, rows_per_group, rows, cols, dtype, dev)
+    got = dict(dh=_new_mat(out.get("dh"), like, shape), do=None, dw_pre=None, dw_post=None, dgate=None)
+    p_dh, p_do, addr = _opt_mat(got["dh"], "out dh", shape, dtype, dev), (None, 0), [None, None, None]
     if o is not None:
-        d_o, lddo = _mat(pick("do"), "out do", shape, like)
-        got["do"] = d_o
-    if w_pre is not None:
-        got["dw_pre"] = _float_vector(out.get("dw_pre"), "dw_pre", (cols,), like)
-    if w_post is not None:
-        got["dw_post"] = _float_vector(out.get("dw_post"), "dw_post", (cols,), like)
-    if gate is not None:
-        got["dgate"] = _float_vector(out.get("dgate"), "dgate", tuple(gate.shape), like)
-    ws_bytes = fp4_norm_residual_backward_workspace_size(rows, cols, w_pre is not None, w_post is not None,
-                                                         gate is not None, per)
-    if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=like.device)
-    fp4_norm_residual_backward(dy, lddy, dh_in, lddhi, h, ldh, o, ldo, in_dtype_of(like), rows, cols, w_post, gate,
-                               ldg, per, alpha, w_pre, rstd_post if w_post is not None else None,
-                               rstd_pre if w_pre is not None else None, dh, lddh, d_o, lddo, got["dw_pre"],
-                               got["dw_post"], got["dgate"], workspace if ws_bytes else None,
-                               workspace.numel() * workspace.element_size() if ws_bytes else 0, stream)
+        got["do"] = _new_mat(out.get("do"), like, shape)
+        p_do = _opt_mat(got["do"], "out do", shape, dtype, dev)
+    for i, (name, has, size) in enumerate((("dw_pre", has_pre, (cols,)), ("dw_post", has_post, (cols,)),
+                                           ("dgate", has_gate, gate_shape))):
+        if has:
+            got[name] = _new_vector(out.get(name), name, size, like, dev)
+            addr[i] = got[name].data_ptr()
+    ws_bytes = fp4_norm_residual_backward_workspace_size(rows, cols, has_pre, has_post, has_gate, gate[2])
+    ws = None
+    if ws_bytes:
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=like.device)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on %s" % like.device)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(_lib.fp4_norm_residual_backward(*p_dy, *p_in, *p_h, *p_o, dt, rows, cols, p_post, *gate, alpha, p_pre, r_post,
+                                           r_pre, *p_dh, *p_do, *addr, ws, ws_bytes, _stream(stream)),
+           "fp4_norm_residual_backward")
     return got

@@ -137,22 +137,28 @@ def test_python_refusals():
 
 
 def test_helper_checks_refuse_wrong_buffers():
-    like = cpu(4, 100)
+    bf16, f32, dev = torch.bfloat16, torch.float32, -1          # -1: CPU tensors, as the checks see them
     good = fp4.alloc_fp8_block(4, 100, device="cpu")
-    assert fp4._fp8_tensor(good, "q", 4, 100, 1, like)[1] == 112
+    assert fp4._fp8_tensor(good, "q", 4, 100, 1, dev)[1] == 112
     for bad in (dict(good, codes=good["codes"][:, :96]), dict(good, codes=good["codes"].t()),
                 dict(good, codes=good["codes"].float()), dict(good, scales=good["scales"][:, ::2]),
                 dict(good, scales=good["scales"][:, :64]), dict(good, lines=5), dict(good, K=99),
                 dict(good, block_lines=128)):
         with pytest.raises((ValueError, TypeError)):
-            fp4._fp8_tensor(bad, "q", 4, 100, 1, like)
+            fp4._fp8_tensor(bad, "q", 4, 100, 1, dev)
+    with pytest.raises((ValueError, TypeError)):
+        fp4._fp8_tensor(good, "q", 4, 100, 1, 0)                # another device
     with pytest.raises(TypeError):
-        fp4._mat(like.float(), "o", (4, 100), like)
+        fp4._mat(cpu(4, 100), "o", (4, 100), f32, dev)
     with pytest.raises(ValueError):
-        fp4._mat(cpu(4, 200)[:, ::2], "o", (4, 100), like)
+        fp4._mat(cpu(4, 200)[:, ::2], "o", (4, 100), bf16, dev)
+    assert fp4._mat(cpu(4, 112)[:, :100], "o", (4, 100), bf16, dev) == 112
+    assert fp4._mat(cpu(1, 100), "o", (1, 100), bf16, dev) == 112    # any pitch does for one row
     with pytest.raises(ValueError):
-        fp4._gate_of(cpu(2, 100), None, 4, 100, like)
+        fp4._gate_of(cpu(2, 100), None, 4, 100, bf16, dev)
     with pytest.raises(ValueError):
-        fp4._gate_of(cpu(3, 100), 2, 4, 100, like)
+        fp4._gate_of(cpu(3, 100), 2, 4, 100, bf16, dev)
     with pytest.raises(ValueError):
-        fp4._float_vector(torch.zeros(5), "rstd", (4,), like)
+        fp4._flat(torch.zeros(5), "rstd", (4,), f32, dev)
+    with pytest.raises(ValueError):
+        fp4._flat(torch.zeros(8)[::2], "rstd", (4,), f32, dev)
