@@ -227,7 +227,6 @@ struct NormArgs {
     float* rstd_pre;
 };
 cudaError_t launch_norm(const NormArgs& a, bool bf16, cudaStream_t s);
-constexpr int NORM_BWD_CTAS = 296;   // two per SM of a B200: partial sums per column
 struct NormBwdArgs {
     const void* dy;
     int64_t lddy;

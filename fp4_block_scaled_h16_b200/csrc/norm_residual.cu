@@ -25,6 +25,8 @@
 // thread reads and writes only its own columns'.  All sums are binary32; h' is
 // rounded before its norm, because the stored h' is what the next block and the
 // backward call see.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -45,7 +47,7 @@ struct Raw {
     uint4 w[BF16 ? 1 : 2];
 };
 
-// the first `n` (1 .. 8) elements of a vector, the others zero
+// the first `n` elements of a vector (8 or more: all; 0 or fewer: none), the others zero
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_raw(const void* p, int n) {
     Raw<BF16> r;
@@ -233,15 +235,6 @@ norm_residual_kernel(const NormArgs a) {
         n[k] = FULL ? VEC : cols - VEC * (tid + k * T);
         off[k] = BYTES * (uint32_t)(tid + k * T);
     }
-    if (a.w_pre) {
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            if (n[k] <= 0) continue;
-            float2 v[PAIRS];
-            widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), v);
-            w_pre.set(tid + k * T, v);
-        }
-    }
     Raw<BF16> hr[VPT], orw[VPT];
     auto fetch = [&](int64_t row) {
         const char* h = row_at<BF16>(a.h, row * a.ldh);
@@ -255,6 +248,15 @@ norm_residual_kernel(const NormArgs a) {
     int64_t grp = -1;
     int turn = 0;
     if ((int64_t)blockIdx.x < a.rows) fetch(blockIdx.x);
+    if (a.w_pre) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (n[k] <= 0) continue;
+            float2 v[PAIRS];
+            widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), v);
+            w_pre.set(tid + k * T, v);
+        }
+    }
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         float2 h[VPT][PAIRS], o[VPT][PAIRS];
 #pragma unroll
@@ -362,38 +364,38 @@ norm_residual_kernel(const NormArgs a) {
 // at its end both dgate = alpha w_post T and dw_post's share, alpha g T, follow.
 // dw_pre and dw_post run over all of a CTA's items.  Partial sums go to the
 // workspace and are added in a fixed order by norm_reduce_kernel, so results do
-// not depend on timing.
+// not depend on timing.  Columns past the row are zeros all the way and are only
+// left out of the stores.
+//
+// Four vectors per thread (beyond 8192 columns) do not fit the registers in this
+// form: there the row's inputs stay as they were loaded, without the next row's,
+// A, n1 and n2 are formed twice, and the sums are in shared memory.
+//
 // FULL as above.  PARTS: which parts of the operator are there, or -1 to ask the
 // arguments.
 constexpr int PART_PRE = 1, PART_RES = 2, PART_POST = 4;
 template <bool BF16, int VPT, int THREADS, bool FULL, int PARTS>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : 2)
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : (THREADS == 128 ? 4 : (VPT == 1 ? 3 : 2)))
 norm_residual_backward_kernel(const NormBwdArgs a) {
     constexpr uint32_t BYTES = VEC * (BF16 ? 2 : 4);
+    constexpr bool BIG = VPT == 4;
+    constexpr int KEPT = BIG ? 1 : VPT;       // vectors whose A, n1, n2 and sums stay in registers
     const bool pre = PARTS < 0 ? a.w_pre != nullptr : (PARTS & PART_PRE) != 0;
     const bool res = PARTS < 0 ? a.o != nullptr : (PARTS & PART_RES) != 0;
     const bool has_post = PARTS < 0 ? a.w_post != nullptr : (PARTS & PART_POST) != 0;
     extern __shared__ float4 columns[];
     __shared__ float4 part[2][32];
     const int tid = (int)threadIdx.x, T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT, warps = T >> 5;
-    const Columns w_pre{columns, vecs}, factor{columns + 2 * vecs, vecs}, post{columns + 4 * vecs, vecs};
+    // BIG: the second and third plane hold the sums of dw_pre and of the item
+    const Columns factor{columns, vecs}, plane1{columns + 2 * vecs, vecs}, plane2{columns + 4 * vecs, vecs};
+    const Columns w_pre = plane1, post = plane2, sum_pre = plane1, sum_item = plane2;
     const float inv_cols = 1.0f / (float)cols;
     int n[VPT];                               // elements of this thread's vectors inside the row
     uint32_t off[VPT];                        // and where they start
-    float2 acc_pre[VPT][PAIRS];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int i = tid + k * T;
-        n[k] = FULL ? VEC : cols - VEC * i;
-        off[k] = BYTES * (uint32_t)i;
-        float2 v[PAIRS];
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) acc_pre[k][e] = v[e] = both(0.0f);
-        post.set(i, v);
-        if (pre && n[k] > 0) {
-            widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), v);
-            w_pre.set(i, v);
-        }
+        n[k] = FULL ? VEC : cols - VEC * (tid + k * T);
+        off[k] = BYTES * (uint32_t)(tid + k * T);
     }
     Raw<BF16> r_dhin[VPT], r_dy[VPT], r_h[VPT], r_o[VPT];
     float rstd2n = 0.0f, rstd1n = 1.0f;
@@ -406,12 +408,37 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
         const char* o = row_at<BF16>(a.o, row * a.ldo);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            r_dhin[k] = a.dh_in && n[k] > 0 ? load_raw<BF16>(dhin + off[k], n[k]) : zero_raw<BF16>();
+            r_dhin[k] = a.dh_in ? load_raw<BF16>(dhin + off[k], n[k]) : zero_raw<BF16>();
             if (pre) {
-                r_dy[k] = n[k] > 0 ? load_raw<BF16>(dy + off[k], n[k]) : zero_raw<BF16>();
-                r_h[k] = n[k] > 0 ? load_raw<BF16>(h + off[k], n[k]) : zero_raw<BF16>();
+                r_dy[k] = load_raw<BF16>(dy + off[k], n[k]);
+                r_h[k] = load_raw<BF16>(h + off[k], n[k]);
             }
-            if (res) r_o[k] = n[k] > 0 ? load_raw<BF16>(o + off[k], n[k]) : zero_raw<BF16>();
+            if (res) r_o[k] = load_raw<BF16>(o + off[k], n[k]);
+        }
+    };
+    // A = dhin + rstd2 a, n2, n1 and d = a of vector k, from the row as loaded
+    float rstd2 = 0.0f, rstd1 = 1.0f;
+    auto form = [&](int k, float2 (&A)[PAIRS], float2 (&n2)[PAIRS], float2 (&n1)[PAIRS], float2 (&d)[PAIRS],
+                    float2 (&dy)[PAIRS]) {
+        widen<BF16>(r_dhin[k], A);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) n2[e] = n1[e] = d[e] = dy[e] = both(0.0f);
+        if (res) widen<BF16>(r_o[k], n1);
+        if (pre) {
+            widen<BF16>(r_h[k], n2);
+            widen<BF16>(r_dy[k], dy);
+            if (BIG) widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), d);
+            else w_pre.get(tid + k * T, d);
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) {
+                n2[e] = __fmul2_rn(n2[e], both(rstd2));
+                d[e] = __fmul2_rn(dy[e], d[e]);
+                A[e] = __ffma2_rn(d[e], both(rstd2), A[e]);
+            }
+        }
+        if (has_post) {
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) n1[e] = __fmul2_rn(n1[e], both(rstd1));
         }
     };
     // the rows of item `it`
@@ -425,63 +452,86 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
     int64_t item = blockIdx.x;
     if (item < a.items) {
         bounds(item, grp, row, last);
-        if (row < last) fetch(row);
+        if (!BIG && row < last) fetch(row);      // on its way before the weights are read
+    }
+    float2 acc_pre[KEPT][PAIRS];
+    float* const post_row = has_post ? a.post_part + (int64_t)blockIdx.x * a.pitch : nullptr;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int i = tid + k * T;
+        float2 v[PAIRS];
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) v[e] = both(0.0f);
+        if (BIG) {
+            sum_pre.set(i, v);
+            if (has_post && n[k] > 0) store_raw<false>(post_row + VEC * i, n[k], narrow<false>(v));
+        } else {
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) acc_pre[BIG ? 0 : k][e] = v[e];
+            post.set(i, v);
+            if (pre) {
+                widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), v);
+                w_pre.set(i, v);
+            }
+        }
     }
     for (; item < a.items; item += gridDim.x) {
         int64_t grp_next = 0, row_next = 0, last_next = 0;
         if (item + gridDim.x < a.items) bounds(item + gridDim.x, grp_next, row_next, last_next);
-        float2 acc[VPT][PAIRS];                    // sum dh' n1
+        float2 acc[KEPT][PAIRS];                   // sum dh' n1
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             float2 f[PAIRS];
 #pragma unroll
-            for (int e = 0; e < PAIRS; ++e) acc[k][e] = both(0.0f);
-            if (n[k] <= 0 || !res) continue;
+            for (int e = 0; e < PAIRS; ++e) {
+                f[e] = both(0.0f);
+                if (!BIG) acc[BIG ? 0 : k][e] = f[e];
+            }
+            if (BIG) sum_item.set(tid + k * T, f);
+            if (!res) continue;
             branch_factor<BF16>(has_post ? a.w_post : nullptr, a.gate, a.ldg, a.alpha, grp, off[k], n[k], f);
             factor.set(tid + k * T, f);
         }
         for (; row < last; ++row) {
-            const float rstd2 = rstd2n, rstd1 = rstd1n;
-            // A = dhin + rstd2 a, n2, n1 and u = alpha g w_post n1: with dh' = A -
-            // rstd2 n2 c1, both means follow from three sums of one pass:
-            // c1 = mean(a n2), c2 = mean(b n1) = mean(u A) - c1 rstd2 mean(u n2)
-            float2 A[VPT][PAIRS], n2[VPT][PAIRS], n1[VPT][PAIRS];
+            if (BIG) fetch(row);
+            rstd2 = rstd2n;
+            rstd1 = rstd1n;
+            // with dh' = A - rstd2 n2 c1, both means follow from three sums of one
+            // pass: c1 = mean(a n2), c2 = mean(b n1) = mean(u A) - c1 rstd2 mean(u n2),
+            // u = alpha g w_post n1
+            float2 A[KEPT][PAIRS], n2[KEPT][PAIRS], n1[KEPT][PAIRS];
             float2 s0 = both(0.0f), s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int i = tid + k * T;
-                widen<BF16>(r_dhin[k], A[k]);
-                if (res) widen<BF16>(r_o[k], n1[k]);
-#pragma unroll
-                for (int e = 0; e < PAIRS; ++e) n2[k][e] = both(0.0f);
-                if (pre && n[k] > 0) {
-                    float2 dy[PAIRS], w[PAIRS];
-                    widen<BF16>(r_h[k], n2[k]);
-                    widen<BF16>(r_dy[k], dy);
-                    w_pre.get(i, w);
+                const int i = tid + k * T, j = BIG ? 0 : k;
+                float2 d[PAIRS], dy[PAIRS];
+                form(k, A[j], n2[j], n1[j], d, dy);
+                if (pre) {
+                    float2 sum[PAIRS];
+                    if (BIG) sum_pre.get(i, sum);
 #pragma unroll
                     for (int e = 0; e < PAIRS; ++e) {
-                        n2[k][e] = __fmul2_rn(n2[k][e], both(rstd2));
-                        acc_pre[k][e] = __ffma2_rn(dy[e], n2[k][e], acc_pre[k][e]);
-                        const float2 d = __fmul2_rn(dy[e], w[e]);
-                        s0 = __ffma2_rn(d, n2[k][e], s0);
-                        A[k][e] = __ffma2_rn(d, both(rstd2), A[k][e]);
+                        if (BIG) sum[e] = __ffma2_rn(dy[e], n2[j][e], sum[e]);
+                        else acc_pre[j][e] = __ffma2_rn(dy[e], n2[j][e], acc_pre[j][e]);
+                        s0 = __ffma2_rn(d[e], n2[j][e], s0);
                     }
+                    if (BIG) sum_pre.set(i, sum);
                 }
-                if (has_post && n[k] > 0) {
+                if (has_post) {
                     float2 f[PAIRS];
                     factor.get(i, f);
 #pragma unroll
                     for (int e = 0; e < PAIRS; ++e) {
-                        n1[k][e] = __fmul2_rn(n1[k][e], both(rstd1));
-                        const float2 u = __fmul2_rn(f[e], n1[k][e]);
-                        s1 = __ffma2_rn(u, A[k][e], s1);
-                        s2 = __ffma2_rn(u, n2[k][e], s2);
+                        const float2 u = __fmul2_rn(f[e], n1[j][e]);
+                        s1 = __ffma2_rn(u, A[j][e], s1);
+                        s2 = __ffma2_rn(u, n2[j][e], s2);
                     }
                 }
             }
-            if (row + 1 < last) fetch(row + 1);
-            else if (row_next < last_next) fetch(row_next);
+            if (!BIG) {
+                if (row + 1 < last) fetch(row + 1);
+                else if (row_next < last_next) fetch(row_next);
+            }
             float c1 = 0.0f, c2 = 0.0f;
             if (pre || has_post) {
                 const float4 sums = block_sum(make_float4(s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, 0.0f), part[turn], tid,
@@ -494,22 +544,29 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
             char* do_out = row_at<BF16>(a.d_o, row * a.lddo);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                if (n[k] <= 0) continue;
+                const int i = tid + k * T, j = BIG ? 0 : k;
+                if (BIG) {
+                    float2 d[PAIRS], dy[PAIRS];
+                    form(k, A[j], n2[j], n1[j], d, dy);
+                }
                 if (pre) {
 #pragma unroll
-                    for (int e = 0; e < PAIRS; ++e) A[k][e] = __ffma2_rn(n2[k][e], both(-c1), A[k][e]);      // dh'
+                    for (int e = 0; e < PAIRS; ++e) A[j][e] = __ffma2_rn(n2[j][e], both(-c1), A[j][e]);      // dh'
                 }
-                store_raw<BF16>(dh_out + off[k], n[k], narrow<BF16>(A[k]));
+                if (n[k] > 0) store_raw<BF16>(dh_out + off[k], n[k], narrow<BF16>(A[j]));
                 if (!res) continue;
-                float2 f[PAIRS];
-                factor.get(tid + k * T, f);
+                float2 f[PAIRS], sum[PAIRS];
+                factor.get(i, f);
+                if (BIG) sum_item.get(i, sum);
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
-                    acc[k][e] = __ffma2_rn(A[k][e], n1[k][e], acc[k][e]);
-                    f[e] = __fmul2_rn(A[k][e], f[e]);                                    // b, or do itself
-                    if (has_post) f[e] = __fmul2_rn(__ffma2_rn(n1[k][e], both(-c2), f[e]), both(rstd1));
+                    if (BIG) sum[e] = __ffma2_rn(A[j][e], n1[j][e], sum[e]);
+                    else acc[j][e] = __ffma2_rn(A[j][e], n1[j][e], acc[j][e]);
+                    f[e] = __fmul2_rn(A[j][e], f[e]);                                    // b, or do itself
+                    if (has_post) f[e] = __fmul2_rn(__ffma2_rn(n1[j][e], both(-c2), f[e]), both(rstd1));
                 }
-                store_raw<BF16>(do_out + off[k], n[k], narrow<BF16>(f));
+                if (BIG) sum_item.set(i, sum);
+                if (n[k] > 0) store_raw<BF16>(do_out + off[k], n[k], narrow<BF16>(f));
             }
         }
         if (a.gate || has_post) {
@@ -517,19 +574,27 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
             for (int k = 0; k < VPT; ++k) {
                 const int i = tid + k * T;
                 if (n[k] <= 0) continue;
-                float2 f[PAIRS];
+                float2 f[PAIRS], sum[PAIRS];
+                if (BIG) {
+                    sum_item.get(i, sum);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < PAIRS; ++e) sum[e] = acc[BIG ? 0 : k][e];
+                }
                 if (has_post) {
                     float2 p[PAIRS];
                     branch_factor<BF16>(nullptr, a.gate, a.ldg, a.alpha, grp, off[k], n[k], f);
-                    post.get(i, p);
+                    if (BIG) widen<false>(load_raw<false>(post_row + VEC * i, n[k]), p);
+                    else post.get(i, p);
 #pragma unroll
-                    for (int e = 0; e < PAIRS; ++e) p[e] = __ffma2_rn(f[e], acc[k][e], p[e]);
-                    post.set(i, p);
+                    for (int e = 0; e < PAIRS; ++e) p[e] = __ffma2_rn(f[e], sum[e], p[e]);
+                    if (BIG) store_raw<false>(post_row + VEC * i, n[k], narrow<false>(p));
+                    else post.set(i, p);
                 }
                 if (a.gate) {
                     branch_factor<BF16>(has_post ? a.w_post : nullptr, nullptr, 0, a.alpha, 0, off[k], n[k], f);
 #pragma unroll
-                    for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], acc[k][e]);
+                    for (int e = 0; e < PAIRS; ++e) f[e] = __fmul2_rn(f[e], sum[e]);
                     float* dst = a.gate_part + item * a.gate_pitch + VEC * i;
                     if (a.gate_pitch % 4 == 0) {
                         store_raw<false>(dst, n[k], narrow<false>(f));
@@ -549,12 +614,19 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
     for (int k = 0; k < VPT; ++k) {
         const int i = tid + k * T;
         if (n[k] <= 0) continue;
-        const int64_t at = (int64_t)blockIdx.x * a.pitch + VEC * i;
-        if (pre) store_raw<false>(a.pre_part + at, n[k], narrow<false>(acc_pre[k]));
-        if (has_post) {
-            float2 p[PAIRS];
-            post.get(i, p);
-            store_raw<false>(a.post_part + at, n[k], narrow<false>(p));
+        float2 v[PAIRS];
+        if (pre) {
+            if (BIG) {
+                sum_pre.get(i, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) v[e] = acc_pre[BIG ? 0 : k][e];
+            }
+            store_raw<false>(a.pre_part + (int64_t)blockIdx.x * a.pitch + VEC * i, n[k], narrow<false>(v));
+        }
+        if (has_post && !BIG) {
+            post.get(i, v);
+            store_raw<false>(post_row + VEC * i, n[k], narrow<false>(v));
         }
     }
 }
@@ -613,6 +685,23 @@ void shape_of(int64_t cols, int& vpt, int& threads) {
     threads = (int)(((nvec + vpt - 1) / vpt + 31) / 32 * 32);
 }
 
+// CTAs of the backward kernel, which have a line of partial sums each: as many as a
+// B200 holds at once, three per SM with up to 256 threads of one vector, two with
+// two, one beyond 4096 columns (4364 x 2034 47 us, 57 with two per SM).  Rows of up
+// to 1024 columns have a form of 128 threads with all their registers and take 512
+// threads per SM: with 768 the longer sum over the lines costs more than the rows
+// gain (1031 x 1003 12.2 us against 14.1).
+int64_t norm_bwd_limit(int64_t cols) {
+    int vpt, threads;
+    shape_of(cols, vpt, threads);
+    if (threads > 256) return 148;
+    return vpt == 1 && threads > 128 ? 444 : 296 * (256 / threads);
+}
+int64_t norm_bwd_ctas(const NormBwdArgs& a) {
+    const int64_t limit = norm_bwd_limit(a.cols);
+    return a.items < limit ? a.items : limit;
+}
+
 template <bool BF16, int VPT, int THREADS, bool FULL, bool RES, bool POST>
 cudaError_t run_norm(const NormArgs& a, int threads, cudaStream_t s) {
     static PerDeviceOnce setup;
@@ -652,7 +741,7 @@ cudaError_t run_norm_bwd(const NormBwdArgs& a, int threads, cudaStream_t s) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(THREADS));
     });
     if (e != cudaSuccess) return e;
-    const int ctas = (int)(a.items < NORM_BWD_CTAS ? a.items : NORM_BWD_CTAS);
+    const int ctas = (int)norm_bwd_ctas(a);
     kernel<<<ctas, threads, smem(threads), s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -664,10 +753,10 @@ cudaError_t run_norm_bwd(const NormBwdArgs& a, int threads, cudaStream_t s) {
 
 template <bool BF16, int VPT, int THREADS, bool FULL>
 cudaError_t run_norm_bwd_parts(const NormBwdArgs& a, int threads, cudaStream_t s) {
-    // the usual blocks compiled for themselves where rows are whole
-    if (FULL && a.w_pre && a.o && a.w_post)
-        return run_norm_bwd<BF16, VPT, THREADS, FULL, FULL ? PART_PRE | PART_RES | PART_POST : -1>(a, threads, s);
-    if (FULL && a.w_pre && a.o) return run_norm_bwd<BF16, VPT, THREADS, FULL, FULL ? PART_PRE | PART_RES : -1>(a, threads, s);
+    // the usual blocks compiled for themselves
+    if (a.w_pre && a.o && a.w_post)
+        return run_norm_bwd<BF16, VPT, THREADS, FULL, PART_PRE | PART_RES | PART_POST>(a, threads, s);
+    if (a.w_pre && a.o) return run_norm_bwd<BF16, VPT, THREADS, FULL, PART_PRE | PART_RES>(a, threads, s);
     return run_norm_bwd<BF16, VPT, THREADS, FULL, -1>(a, threads, s);
 }
 
@@ -686,6 +775,8 @@ template <bool BF16, class Args>
 cudaError_t launch_columns(const Args& a, cudaStream_t s) {
     int vpt, threads;
     shape_of(a.cols, vpt, threads);
+    if constexpr (std::is_same<Args, NormBwdArgs>::value)
+        if (threads <= 128) return launch_shape<BF16, 1, 128>(a, threads, s);
     if (vpt == 1) return launch_shape<BF16, 1, 256>(a, threads, s);
     if (vpt == 4) return launch_shape<BF16, 4, 512>(a, threads, s);
     return threads <= 256 ? launch_shape<BF16, 2, 256>(a, threads, s) : launch_shape<BF16, 2, 512>(a, threads, s);
@@ -697,7 +788,7 @@ void norm_bwd_plan(NormBwdArgs& a) {
     a.groups = a.gate ? (a.rows + a.per - 1) / a.per : 1;
     if (!a.gate) a.per = a.rows;
     // segments per group: enough items for every CTA, each of at least one row
-    int64_t nseg = (NORM_BWD_CTAS + a.groups - 1) / a.groups;
+    int64_t nseg = (norm_bwd_limit(a.cols) + a.groups - 1) / a.groups;
     if (nseg > a.per) nseg = a.per;
     a.seg_rows = (a.per + nseg - 1) / nseg;
     a.nseg = (a.per + a.seg_rows - 1) / a.seg_rows;
@@ -706,7 +797,7 @@ void norm_bwd_plan(NormBwdArgs& a) {
 }
 
 size_t norm_bwd_workspace(const NormBwdArgs& a) {
-    const int64_t ctas = a.items < NORM_BWD_CTAS ? a.items : NORM_BWD_CTAS;
+    const int64_t ctas = norm_bwd_ctas(a);
     const int64_t lines = (a.w_pre ? ctas : 0) + (a.w_post ? ctas : 0) + ((a.gate && a.nseg > 1) ? a.items : 0);
     return (size_t)lines * (size_t)a.pitch * sizeof(float);
 }
@@ -716,7 +807,7 @@ cudaError_t launch_norm(const NormArgs& a, bool bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_bwd(NormBwdArgs a, bool bf16, float* workspace, cudaStream_t s) {
-    const int64_t ctas = a.items < NORM_BWD_CTAS ? a.items : NORM_BWD_CTAS;
+    const int64_t ctas = norm_bwd_ctas(a);
     a.pre_part = workspace;
     a.post_part = a.pre_part + (a.w_pre ? ctas * a.pitch : 0);
     // one item per group: its sums are dgate's row
