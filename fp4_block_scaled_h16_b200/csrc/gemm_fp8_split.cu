@@ -52,15 +52,21 @@ struct SCfg {
     static constexpr uint32_t N_BYTES = NT * BK;
     static constexpr uint32_t SN_BYTES = NT * 4;          // scales of the tile's N side
     static constexpr uint32_t SL_BYTES = LANES * 4;       // ... and of its lanes
-    static constexpr uint32_t STAGE_BYTES = (L_BYTES + N_BYTES + SN_BYTES + SL_BYTES + 1023) / 1024 * 1024;
+    static constexpr uint32_t STAGE_BYTES = L_BYTES + N_BYTES;
+    static constexpr uint32_t SC_BYTES = SN_BYTES + SL_BYTES;
     static constexpr uint32_t EXTRA = 1024 + 512;         // alignment, barriers
-    static constexpr int STAGES = (int)((232448u / CTAS - 1024u - EXTRA) / STAGE_BYTES);
+    static constexpr int PBUF = WIDE ? 2 : 4;             // TMEM buffers of NT columns
+    // Scales have a longer ring, without barriers of its own, so that a stage is
+    // free when its MMAs are done: they were issued once the promotion had read the
+    // partial PBUF chunks before, and so was past the scales of the chunk before that.
+    static constexpr int STAGES =
+        (int)((232448u / CTAS - 1024u - EXTRA - (PBUF + 1) * SC_BYTES) / (STAGE_BYTES + SC_BYTES));
+    static constexpr int SC_SLOTS = STAGES + PBUF + 1;
     // the partial tile, over the stages: rows of C (NT lines of A, or 128), padded
     // so that eight rows' 16-byte chunks differ in bank
     static constexpr int RED_PITCH = (WIDE ? NT : LANES) + 4;
     static constexpr uint32_t RED_BYTES = (WIDE ? LANES : NT) * RED_PITCH * 4;
-    static constexpr uint32_t SMEM = STAGES * STAGE_BYTES + EXTRA;
-    static constexpr int PBUF = WIDE ? 2 : 4;        // TMEM buffers of NT columns
+    static constexpr uint32_t SMEM = STAGES * STAGE_BYTES + SC_SLOTS * SC_BYTES + EXTRA;
     static constexpr uint32_t TMEM_COLS = PBUF * NT;
     static_assert(RED_BYTES <= STAGES * STAGE_BYTES, "the partial tile fits over the ring");
     static_assert(TMEM_COLS >= 32 && TMEM_COLS * CTAS <= 512, "TMEM of an SM's CTAs");
@@ -122,6 +128,50 @@ __device__ __forceinline__ void all_roles() {
     asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// The sum over the ranks of a cluster of their partial tiles `red`, in rank order,
+// for the rows of C that are this rank's.  RANKS is a bound on `ranks`; eight loads
+// are in flight per thread, because a load from another CTA waits long
+// (one by one 333 x 4096 x 512 takes 9.6 us, 9.0 this way).
+template <int SPANS, int PITCH, int WARPS, bool OUT_BF16>
+struct Reduce {
+    template <int RANKS>
+    static __device__ __forceinline__ void rows(const SplitParams& p, const float* red, int rank, int ranks, int rows,
+                                                int cols, int64_t at0) {
+        constexpr int U = 8 / RANKS;                 // (row, span) steps of a warp at a time
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int i = warp; rank + i / SPANS * ranks < rows; i += U * WARPS) {
+            float4 part[U][RANKS];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = i + u * WARPS, row = rank + k / SPANS * ranks, col = k % SPANS * 128 + 4 * lane;
+                const bool in = row < rows && col < cols;
+                const float* at = red + row * PITCH + col;
+#pragma unroll
+                for (int r = 0; r < RANKS; ++r) {
+                    if (!in || r >= ranks) continue;
+                    if (RANKS == 1) part[u][r] = *reinterpret_cast<const float4*>(at);
+                    else part[u][r] = ld_cluster_v4(sm100::cluster_addr(at, (uint32_t)r));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = i + u * WARPS, row = rank + k / SPANS * ranks, col = k % SPANS * 128 + 4 * lane;
+                if (row >= rows || col >= cols) continue;
+                float4 v = part[u][0];
+#pragma unroll
+                for (int r = 1; r < RANKS; ++r)
+                    if (r < ranks) {
+                        v.x += part[u][r].x;
+                        v.y += part[u][r].y;
+                        v.z += part[u][r].z;
+                        v.w += part[u][r].w;
+                    }
+                put4<OUT_BF16>(p.c, at0 + (int64_t)row * p.ldc + col, v, cols - col);
+            }
+        }
+    }
+};
+
 // SWAP: lanes are lines of B and the N side rows of A, else the reverse.
 // VEC: B's scales are one per line (1 x 128 blocks), else one per 128 lines.
 template <int NT, bool SWAP, bool VEC, bool OUT_BF16>
@@ -134,7 +184,8 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = sm100::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::STAGES * G::STAGE_BYTES);
+    uint8_t* sc_ring = smem + G::STAGES * G::STAGE_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sc_ring + G::SC_SLOTS * G::SC_BYTES);
     uint64_t* empty = full + G::STAGES;
     uint64_t* pfull = empty + G::STAGES;
     uint64_t* pempty = pfull + G::PBUF;
@@ -150,7 +201,7 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::STAGES; ++s) {
             sm100::mbar_init(&full[s], 1);
-            sm100::mbar_init(&empty[s], 1 + G::PROMO_WARPS);   // the MMAs, and the readers of the scales
+            sm100::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < G::PBUF; ++b) {
             sm100::mbar_init(&pfull[b], 1);
@@ -186,7 +237,7 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
             const int64_t lpl = SWAP ? p.lpb : p.lpa, lpn = SWAP ? p.lpa : p.lpb;
             // lines past M and N lie in the scale rows' padding to 128
             const uint32_t sn_bytes = !N_VEC ? 0u : (uint32_t)min((int64_t)NT, lpn - t0) * 4u;
-            int stage = 0;
+            int stage = 0, slot = 0;
             uint32_t phase = 0, fills = 0;
             for (int kc = kc0; kc < kc1; ++kc) {
                 if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, p.wait_limit, abort_flag)) {
@@ -194,15 +245,15 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
                     break;
                 }
                 uint8_t* st = smem + stage * G::STAGE_BYTES;
+                uint8_t* sc = sc_ring + slot * G::SC_BYTES;
                 sm100::mbar_arrive_expect_tx(&full[stage],
                                              G::L_BYTES + G::N_BYTES + sn_bytes + (LANE_VEC ? G::SL_BYTES : 0u));
                 sm100::tma_load_2d(st, &tmL, kc * BK, l0, &full[stage]);
                 sm100::tma_load_2d(st + G::L_BYTES, &tmN, kc * BK, t0, &full[stage]);
-                if (N_VEC) sm100::bulk_load(st + G::L_BYTES + G::N_BYTES, sn + kc * lpn + t0, sn_bytes, &full[stage]);
-                if (LANE_VEC)
-                    sm100::bulk_load(st + G::L_BYTES + G::N_BYTES + G::SN_BYTES, sl + kc * lpl + l0, G::SL_BYTES,
-                                     &full[stage]);
+                if (N_VEC) sm100::bulk_load(sc, sn + kc * lpn + t0, sn_bytes, &full[stage]);
+                if (LANE_VEC) sm100::bulk_load(sc + G::SN_BYTES, sl + kc * lpl + l0, G::SL_BYTES, &full[stage]);
                 ++fills;
+                if (++slot == G::SC_SLOTS) slot = 0;
                 if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
             }
             for (int s = 0; s < G::STAGES; ++s)
@@ -252,21 +303,22 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
         float2 acc[G::WC / 2];
 #pragma unroll
         for (int c = 0; c < G::WC / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-        int stage = 0, pb = 0;
-        uint32_t phase = 0, pphase = 0;
+        int slot = 0, pb = 0;
+        uint32_t pphase = 0;
+        bool seen = false;
         // columns past N take the last block's scale; they are not stored
         const float* sb_block = p.sb + (VEC ? 0 : min((int64_t)(SWAP ? l0 : t0 + n0) / 128, p.lpb - 1));
         float sb32 = 0.0f;                          // lane l: the block scale of chunk kc0 + 32 i + l
         for (int kc = kc0; kc < kc1; ++kc) {
             if (!VEC && ((kc - kc0) & 31) == 0) sb32 = __ldg(sb_block + min(kc + lane, kc1 - 1) * p.lpb);
-            const bool ok = sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag) &&
-                            sm100::mbar_wait(&full[stage], phase, p.wait_limit, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
+            if (!__all_sync(0xffffffffu, seen) &&
+                !__all_sync(0xffffffffu, sm100::mbar_wait(&pfull[pb], pphase, p.wait_limit, abort_flag))) {
                 if (lane == 0) raise_timeout(p, abort_flag);
                 break;
             }
             sm100::tc_fence_after();
-            const float* sn = reinterpret_cast<const float*>(smem + stage * G::STAGE_BYTES + G::L_BYTES + G::N_BYTES);
+            // the chunk's scales landed before its MMAs ran
+            const float* sn = reinterpret_cast<const float*>(sc_ring + slot * G::SC_BYTES);
             float s = LANE_VEC ? sn[NT + 32 * q + lane] : 1.0f;
             if (!VEC) s = __fmul_rn(s, __shfl_sync(0xffffffffu, sb32, (kc - kc0) & 31));
             const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + NT * pb + n0;
@@ -285,7 +337,9 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
                 if (c0 + F * W == G::WC) {
                     sm100::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) sm100::mbar_arrive(&pempty[pb]);
+                    if (lane == 0) sm100::mbar_arrive_cluster_relaxed(sm100::smem_u32(&pempty[pb]));
+                    if (++pb == G::PBUF) { pb = 0; pphase ^= 1u; }
+                    seen = sm100::mbar_test_wait(&pfull[pb], pphase);    // the next chunk's, ahead of the sums
                 }
 #pragma unroll
                 for (int c = 0; c < F * W; c += 4) {
@@ -301,10 +355,7 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
                     d[1] = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), w1, d[1]);
                 }
             }
-            __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(&empty[stage]);
-            if (++stage == G::STAGES) { stage = 0; phase ^= 1u; }
-            if (++pb == G::PBUF) { pb = 0; pphase ^= 1u; }
+            if (++slot == G::SC_SLOTS) slot = 0;
         }
         // every load and MMA of this CTA has completed once all roles are here, so
         // the partial tile may take the ring's place
@@ -331,31 +382,11 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
     // the ranks of a cluster share the rows of C; a warp takes 128 columns of a
     // row at a time, four per thread
     const int64_t at0 = (int64_t)(SWAP ? t0 : l0) * p.ldc + (SWAP ? l0 : t0);
-    constexpr int SPANS = (SWAP ? LANES : NT) / 128;
-    for (int i = warp; rank + i / SPANS * ranks < rows; i += G::THREADS / 32) {
-        const int row = rank + i / SPANS * ranks, col = i % SPANS * 128 + 4 * lane;
-        if (col >= cols) continue;
-        const float* at = red + row * G::RED_PITCH + col;
-        float4 v;
-        if (ranks == 1) {
-            v = *reinterpret_cast<const float4*>(at);
-        } else {
-            float4 part[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < ranks) part[r] = ld_cluster_v4(sm100::cluster_addr(at, (uint32_t)r));
-            v = part[0];
-#pragma unroll
-            for (int r = 1; r < 8; ++r)
-                if (r < ranks) {
-                    v.x += part[r].x;
-                    v.y += part[r].y;
-                    v.z += part[r].z;
-                    v.w += part[r].w;
-                }
-        }
-        put4<OUT_BF16>(p.c, at0 + (int64_t)row * p.ldc + col, v, cols - col);
-    }
+    using Red = Reduce<(SWAP ? LANES : NT) / 128, G::RED_PITCH, G::THREADS / 32, OUT_BF16>;
+    if (ranks == 1) Red::template rows<1>(p, red, rank, ranks, rows, cols, at0);
+    else if (ranks == 2) Red::template rows<2>(p, red, rank, ranks, rows, cols, at0);
+    else if (ranks <= 4) Red::template rows<4>(p, red, rank, ranks, rows, cols, at0);
+    else Red::template rows<8>(p, red, rank, ranks, rows, cols, at0);
     if (ranks > 1) sm100::cluster_sync();                    // no CTA leaves while another reads its tile
     if (warp == 1) {
         __syncwarp();
