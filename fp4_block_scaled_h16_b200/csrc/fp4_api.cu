@@ -722,11 +722,17 @@ fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float
     g.M = M; g.N = N; g.K = K; g.c = c; g.ldc = ldc;
     g.out_bf16 = out_dtype == FP4_OUT_BF16;
     g.wait_limit = g_wait_limit;
-    // While the 128 x 256 tiles leave at least half of the SMs to a split of K, the
-    // split kernel is faster, beyond that the pair tiles are: 384 x 6144 x 4096
-    // (72 tiles) 18.9 and 22.1 us, 512 x 6144 x 4096 (96 tiles) 24.1 and 22.2 us.
+    // The split kernel has one 128 x 256 tile per CTA, or a share of one's K while
+    // the tiles leave half of the SMs idle; the pair kernel has 256 x 256 tiles on
+    // two SMs and costs 7 / 8 of the time per round of tiles.  At K = 4096, 256 x
+    // 28672 (two rounds each) takes 43.9 us split and 39.7 on pairs, 640 x 14336 (two
+    // rounds, three) 42.8 and 54.7, 1152 x 4096 (one, two) 21.9 and 38.0, and 128 x
+    // 28672, which fills half of a pair's tile, 28.5 and 39.4.
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool pairs = g_gemm_pairs && M > 64 && ((M + 127) / 128) * ((N + 255) / 256) * 2 > num_sms();
+    const int64_t sms = num_sms(), tiles_n = (N + 255) / 256;
+    const int64_t tiles = (M + 127) / 128 * tiles_n, pair_tiles = (M + 255) / 256 * tiles_n;
+    const int64_t rounds = (tiles + sms - 1) / sms, pair_rounds = (pair_tiles + sms / 2 - 1) / (sms / 2);
+    const bool pairs = g_gemm_pairs && M > 64 && tiles * 2 > sms && 7 * pair_rounds <= 8 * rounds;
     if ((pairs ? launch_gemm_fp8_pair(g, s) : launch_gemm_fp8_split(g, s)) != cudaSuccess) return FP4_ERR_CUDA;
     return FP4_OK;
 }

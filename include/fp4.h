@@ -608,9 +608,9 @@ void fp4_set_wait_limit(uint32_t polls);
  * 256 x 256 output tiles shared by two SMs through tcgen05 cta_group::2, each
  * SM loading its own A rows and half of B (nonzero, the default), or on single
  * CTAs with 128 x 256 tiles (0).  The products are the same block-scaled dot
- * products either way.  It selects the same for fp4_fp8_block_gemm: 256 x 256
- * tiles on pairs where they fill the GPU, or 128-line tiles with K split.  Process-wide; not synchronized with calls in flight on
- * other host threads.
+ * products either way.  For fp4_fp8_block_gemm 0 rules the 256 x 256 tiles on
+ * pairs out; by default they run where they finish sooner than 128-row tiles.
+ * Process-wide; not synchronized with calls in flight on other host threads.
  */
 void fp4_set_gemm_cta_pairs(int enable);
 
