@@ -728,6 +728,8 @@ def norm_residual_backward(dy, h, rstd_pre=None, w_pre=None, dh_in=None, o=None,
     if ws_bytes:
         if workspace is None:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=like.device)
+            if stream is not None:       # it returns to the current stream's pool while `stream` may still use it
+                workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), like.device))
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous and on %s" % like.device)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -7,8 +7,9 @@ and 16 warps: 53 roundings, and the mean, eps, square root and reciprocal 4
 more, halved by the square root in an inverse RMS: 31.  With the products after
 it the forward results stay under 40 u.  Backward, a mean of products takes 56
 and the values in it up to 6: 70 u for dh; do adds a second such mean of values
-that are off by 70 u: 140 u.  A column sum adds at most rows / 296 + 1 rows in a
-CTA and 296 / 8 + 8 partial sums, 60 for the sizes here: 80 u for dw_pre, 220 u
+that are off by 70 u: 140 u.  A column sum adds, per CTA, the rows that 148
+CTAs or more leave to it, 5 for up to 700 rows, and then every 32nd of at most
+700 partial sums and 32 such, 54: 60 for the sizes here, 80 u for dw_pre, 220 u
 for dw_post and dgate, whose terms hold dh.  A result in bf16 adds half a step,
 2^-8 of it.
 """
@@ -217,3 +218,34 @@ def test_gradients_do_not_depend_on_timing(fp4):
     for _ in range(3):
         again = run()
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_own_workspace_on_another_stream(fp4, monkeypatch):
+    """The workspace that the helper allocates is not handed out again before the
+    call has run on its stream."""
+    a = inputs(600, 1024, torch.bfloat16, True, 200, 0, 77)
+    f = fp4.norm_residual(alpha=0.5, rows_per_group=200, **a)
+    dy = matrix(torch.Generator().manual_seed(78), 600, 1024, torch.bfloat16)
+    kw = dict(rstd_pre=f["rstd_pre"], w_pre=a["w_pre"], o=a["o"], w_post=a["w_post"], rstd_post=f["rstd_post"],
+              gate=a["gate"], rows_per_group=200, alpha=0.5)
+    want = fp4.norm_residual_backward(dy, f["h"], **kw)
+    size = fp4.fp4_norm_residual_backward_workspace_size(600, 1024, True, True, True, 200)
+    used, call = [], fp4._lib.fp4_norm_residual_backward
+
+    def spy(*args):
+        used.append(args[-3])
+        return call(*args)
+    monkeypatch.setattr(fp4._lib, "fp4_norm_residual_backward", spy)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        out = {k: torch.empty_like(v) for k, v in want.items()}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)            # tens of milliseconds
+        got = fp4.norm_residual_backward(dy, f["h"], out=out, stream=stream, **kw)
+        others = [torch.full((size,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        assert not side.query()                      # all of them were handed out before the call ran
+        assert used[-1] not in [t.data_ptr() for t in others]
+        torch.cuda.synchronize()
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
