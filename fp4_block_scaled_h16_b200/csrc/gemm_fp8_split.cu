@@ -87,6 +87,7 @@ struct SplitParams {
     void* c;
     int64_t ldc;
     int M, N, chunks;
+    int lane_tile0, n_tile0;  // the first tile of a launch
     uint32_t wait_limit;
     unsigned int* err;
 };
@@ -203,7 +204,7 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;      // the cluster spans the x dimension
-    const int l0 = (int)blockIdx.y * LANES, t0 = (int)blockIdx.z * NT;
+    const int l0 = (p.lane_tile0 + (int)blockIdx.y) * LANES, t0 = (p.n_tile0 + (int)blockIdx.z) * NT;
     const int kc0 = (int)((int64_t)p.chunks * rank / ranks), kc1 = (int)((int64_t)p.chunks * (rank + 1) / ranks);
 
     // one thread's loads of chunk kc
@@ -460,9 +461,19 @@ cudaError_t run_split(const Fp8GemmArgs& g, cudaStream_t s) {
     p.chunks = (int)chunks;
     p.wait_limit = g.wait_limit;
     p.err = device_error_word();
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)((lanes + LANES - 1) / LANES), (unsigned)((cols + NT - 1) / NT));
     attr.val.clusterDim.x = (unsigned)ranks;
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_split_kernel<NT, SWAP, VEC, OUT_BF16>, SWAP ? tb : ta, SWAP ? ta : tb, p);
+    // one launch, unless a side has more tiles than a grid has lines
+    constexpr int MAX_LINES = 65535;
+    const int lane_tiles = (int)((lanes + LANES - 1) / LANES), n_tiles = (int)((cols + NT - 1) / NT);
+    for (p.n_tile0 = 0; p.n_tile0 < n_tiles; p.n_tile0 += MAX_LINES)
+        for (p.lane_tile0 = 0; p.lane_tile0 < lane_tiles; p.lane_tile0 += MAX_LINES) {
+            cfg.gridDim = dim3((unsigned)ranks, (unsigned)min(lane_tiles - p.lane_tile0, MAX_LINES),
+                               (unsigned)min(n_tiles - p.n_tile0, MAX_LINES));
+            const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp8_split_kernel<NT, SWAP, VEC, OUT_BF16>,
+                                                     SWAP ? tb : ta, SWAP ? ta : tb, p);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
 }
 
 template <int NT, bool SWAP>

@@ -184,6 +184,47 @@ def test_gemm_wait_timeout_is_reported_and_recoverable(fp4, M, N, K, b_lines):
     assert torch.equal(before, after)
 
 
+@pytest.mark.parametrize("b_lines", [1, 128])
+def test_quantizer_recovers_from_a_wait_that_runs_out(fp4, b_lines):
+    """One poll may or may not see the tile land; a call after it is right either way."""
+    x = torch.randn((1500, 2100), generator=torch.Generator().manual_seed(6)).cuda()
+    for t in (x, x.bfloat16()):
+        t = torch.nn.functional.pad(t, (0, 12))[:, :2100]
+        before = fp4.fp8_block_quantize_both_axes(t, b_lines)
+        fp4.fp4_set_wait_limit(1)
+        try:
+            fp4.fp8_block_quantize_both_axes(t, b_lines)
+            status = fp4.fp4_last_error()
+        finally:
+            fp4.fp4_set_wait_limit(0)
+        assert status in (fp4.FP4_OK, fp4.FP4_ERR_TIMEOUT), fp4.fp4_status_string(status)
+        after = fp4.fp8_block_quantize_both_axes(t, b_lines)
+        assert fp4.fp4_last_error() == fp4.FP4_OK
+        for a, b, n, k in zip(before, after, (1500, 2100), (2100, 1500)):
+            assert torch.equal(a["codes"][:, :k], b["codes"][:, :k])
+            m = n if b_lines == 1 else a["scales"].shape[1]
+            assert torch.equal(a["scales"][:, :m], b["scales"][:, :m])
+
+
+@pytest.mark.parametrize("M,N,out", [(3, 128 * 65536 + 40, "bf16"), (128 * 65536 + 40, 3, "f32")])
+def test_gemm_with_more_tiles_than_a_grid_has_lines(fp4, M, N, out):
+    """Beyond 65535 tiles along either side, on single CTAs."""
+    K = 16
+    g = torch.Generator(device="cuda").manual_seed(7)
+    a = torch.randint(-3, 4, (M, K), generator=g, device="cuda").to(torch.bfloat16)
+    b = torch.randint(-3, 4, (N, K), generator=g, device="cuda").to(torch.bfloat16)
+    a[:, 0] = b[:, 0] = 7                                    # one scale, 7 / 448 = 2^-6, for every block
+    qa, qb = fp4.fp8_block_quantize(a), fp4.fp8_block_quantize(b)
+    fp4.fp4_set_gemm_cta_pairs(False)
+    try:
+        c = fp4.fp8_block_gemm(qa, qb, fp4.FP4_OUT_BF16 if out == "bf16" else fp4.FP4_OUT_F32)
+    finally:
+        fp4.fp4_set_gemm_cta_pairs(True)
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+    want = a.float() @ b.float().T                           # integers below 2^8: exact
+    assert torch.equal(c.float(), want)
+
+
 def test_two_streams_at_once(fp4):
     g = torch.Generator().manual_seed(4)
     x, w = torch.randn((64, 4096), generator=g).cuda(), torch.randn((1024, 4096), generator=g).cuda()
