@@ -727,12 +727,15 @@ fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float
     // two SMs and costs 7 / 8 of the time per round of tiles.  At K = 4096, 256 x
     // 28672 (two rounds each) takes 43.9 us split and 39.7 on pairs, 640 x 14336 (two
     // rounds, three) 42.8 and 54.7, 1152 x 4096 (one, two) 21.9 and 38.0, and 128 x
-    // 28672, which fills half of a pair's tile, 28.5 and 39.4.
+    // 28672, which fills half of a pair's tile, 28.5 and 39.4.  With 1 x 128 blocks of
+    // B a single round of the split kernel's 128 x 192 tiles is faster than either:
+    // 512 x 6144 x 4096 24.3 us, 27.4 on pairs.
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t sms = num_sms(), tiles_n = (N + 255) / 256;
     const int64_t tiles = (M + 127) / 128 * tiles_n, pair_tiles = (M + 255) / 256 * tiles_n;
     const int64_t rounds = (tiles + sms - 1) / sms, pair_rounds = (pair_tiles + sms / 2 - 1) / (sms / 2);
-    const bool pairs = g_gemm_pairs && M > 64 && tiles * 2 > sms && 7 * pair_rounds <= 8 * rounds;
+    const bool one_round = b_block_lines == 1 && (M + 127) / 128 * ((N + 191) / 192) <= sms;
+    const bool pairs = g_gemm_pairs && M > 64 && tiles * 2 > sms && 7 * pair_rounds <= 8 * rounds && !one_round;
     if ((pairs ? launch_gemm_fp8_pair(g, s) : launch_gemm_fp8_split(g, s)) != cudaSuccess) return FP4_ERR_CUDA;
     return FP4_OK;
 }

@@ -8,7 +8,7 @@
 // With few tokens the call is bound by reading the weight B once.  So the
 // roles are swapped: a tile is 128 lines of B (the M of the MMA, one TMEM lane
 // each) by NT rows of A (its N, 16 to 64), two CTAs per SM.  Beyond 64 rows a
-// tile is 128 rows of A (the lanes) by 256 lines of B.  K is split over a
+// tile is 128 rows of A (the lanes) by 256 lines of B, or 192.  K is split over a
 // cluster of up to eight CTAs.  Each 128-K chunk is four kind::f8f6f4 MMAs into
 // one of several TMEM buffers; four warps (eight for 256 lines) promote it,
 // acc += P (sA sB), in binary32 registers, because an FP32 scale per chunk
@@ -18,11 +18,12 @@
 //
 // One token, N = 6144, K = 4096: 7.25 us, 25 MB of weights at 3470 GB/s; about
 // half of it is the launch, the first loads' latency and the sum over the
-// cluster.  333 x 4096 x 14336 (three CTAs per tile): 32.7 us, 1200 TFLOP/s.  A
-// chunk takes 0.64 us there, of which the loads alone would take 0.49 (48 KB per
-// CTA and chunk, 14 TB/s out of L2) and the MMAs alone 0.42; 5 us are the sum over
-// the cluster, at the rate of distributed shared memory.  Tiles of 128 x 128 with
-// two CTAs per SM: 40 us.
+// cluster.  333 x 4096 x 14336: 32.7 us, 1200 TFLOP/s, on 48 clusters of two (the
+// GPU holds 45 of three).  A chunk takes 0.42 us there, of which the loads alone
+// would take 0.33 (264 MB out of L2 for all tiles, 14 TB/s) and the MMAs alone
+// 0.28; 9 us are the launch, the first loads and the sum over the cluster, 2.6 of
+// them at the rate of distributed shared memory.  Tiles of 128 x 128 with two CTAs
+// per SM: 40 us.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (and TMEM), warps 2-5
 // promotion; for 256 lines of B two issuers, and promotion by warps 4-11 with
@@ -49,7 +50,7 @@ constexpr unsigned int ERR_TIMEOUT = 7u;
 
 template <int NT>
 struct SCfg {
-    static constexpr bool WIDE = NT == 256;
+    static constexpr bool WIDE = NT > 64;
     static constexpr int MMA_WARPS = WIDE ? 2 : 1;        // issuers, which take the chunks in turn
     static constexpr int FIRST = WIDE ? 4 : 2;            // first promotion warp
     static constexpr int PROMO_WARPS = WIDE ? 8 : 4;
@@ -75,7 +76,8 @@ struct SCfg {
     static constexpr int RED_PITCH = (WIDE ? NT : LANES) + 4;
     static constexpr uint32_t RED_BYTES = (WIDE ? LANES : NT) * RED_PITCH * 4;
     static constexpr uint32_t SMEM = STAGES * STAGE_BYTES + SC_SLOTS * SC_BYTES + EXTRA;
-    static constexpr uint32_t TMEM_COLS = PBUF * NT;
+    static constexpr uint32_t PSTRIDE = WIDE ? 256 : NT;    // TMEM columns from buffer to buffer
+    static constexpr uint32_t TMEM_COLS = PBUF * PSTRIDE;
     static_assert(RED_BYTES <= STAGES * STAGE_BYTES, "the partial tile fits over the ring");
     static_assert(TMEM_COLS >= 32 && TMEM_COLS * CTAS <= 512, "TMEM of an SM's CTAs");
 };
@@ -296,7 +298,7 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
                     const uint64_t dl = sm100::desc_sw128(st), dn = sm100::desc_sw128(st + G::L_BYTES);
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk)
-                        sm100::mma_f8(tmem + NT * pb, dl + 2 * kk, dn + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                        sm100::mma_f8(tmem + G::PSTRIDE * pb, dl + 2 * kk, dn + 2 * kk, idesc, kk > 0 ? 1u : 0u);
                     issued = true;
                     sm100::tc_commit(&pfull[pb]);
                     sm100::tc_commit(&empty[stage]);
@@ -336,9 +338,9 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
             const float* sn = reinterpret_cast<const float*>(sc_ring + slot * G::SC_BYTES);
             float s = LANE_VEC ? sn[NT + 32 * q + lane] : 1.0f;
             if (!VEC) s = __fmul_rn(s, __shfl_sync(0xffffffffu, sb32, (kc - kc0) & 31));
-            const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + NT * pb + n0;
+            const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + G::PSTRIDE * pb + n0;
             constexpr int W = G::WC < 32 ? 16 : 32;             // columns per TMEM load
-            constexpr int F = G::WC > W ? 2 : 1;                // loads in flight
+            constexpr int F = G::WC % 96 == 0 ? 3 : (G::WC > W ? 2 : 1);   // loads in flight
 #pragma unroll
             for (int c0 = 0; c0 < G::WC; c0 += F * W) {
                 uint32_t r[F][W];
@@ -397,7 +399,7 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
     // the ranks of a cluster share the rows of C; a warp takes 128 columns of a
     // row at a time, four per thread
     const int64_t at0 = (int64_t)(SWAP ? t0 : l0) * p.ldc + (SWAP ? l0 : t0);
-    using Red = Reduce<(SWAP ? LANES : NT) / 128, G::RED_PITCH, G::THREADS / 32, OUT_BF16>;
+    using Red = Reduce<(SWAP ? LANES : NT + 127) / 128, G::RED_PITCH, G::THREADS / 32, OUT_BF16>;
     if (ranks == 1) Red::template rows<1>(p, red, rank, ranks, rows, cols, at0);
     else if (ranks == 2) Red::template rows<2>(p, red, rank, ranks, rows, cols, at0);
     else if (ranks <= 4) Red::template rows<4>(p, red, rank, ranks, rows, cols, at0);
@@ -410,8 +412,9 @@ gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_cons
     }
 }
 
+// launches the product, or only tells what it would cost
 template <int NT, bool SWAP, bool VEC, bool OUT_BF16>
-cudaError_t run_split(const Fp8GemmArgs& g, cudaStream_t s) {
+cudaError_t run_split(const Fp8GemmArgs& g, cudaStream_t s, int64_t* cost = nullptr) {
     using G = SCfg<NT>;
     static PerDeviceOnce setup;
     static int max_clusters[kOnceDevices][MAX_RANKS + 1] = {};   // resident at once, one CTA per SM, by cluster size
@@ -445,6 +448,10 @@ cudaError_t run_split(const Fp8GemmArgs& g, cudaStream_t s) {
     int ranks = 1;
     for (int r = 2; r <= MAX_RANKS; ++r)
         if (tiles <= G::CTAS * max_clusters[dev][r] && chunks >= 2 * r) ranks = r;
+    if (cost) {                             // columns of all chunks that the busiest SM promotes
+        *cost = (tiles * ranks + num_sms() - 1) / num_sms() * ((chunks + ranks - 1) / ranks) * NT;
+        return cudaSuccess;
+    }
     CUtensorMap ta, tb;
     if (!make_fp8_map(&ta, g.a_codes, g.M, g.K, g.lda, SWAP ? NT : LANES) ||
         !make_fp8_map(&tb, g.b_codes, g.N, g.K, g.ldb, SWAP ? LANES : NT))
@@ -483,13 +490,28 @@ cudaError_t run_nt(const Fp8GemmArgs& g, cudaStream_t s) {
     return g.out_bf16 ? run_split<NT, SWAP, false, true>(g, s) : run_split<NT, SWAP, false, false>(g, s);
 }
 
+// With 1 x 128 blocks of B the promotion, one product per element more, bounds a
+// chunk, not its loads, so tiles of 192 lines gain where they spread over more SMs:
+// 333 x 4096 x 14336 44.1 -> 37.6 us, 512 x 6144 x 4096 28.0 -> 24.3, but 300 x
+// 6144 x 4096 20.2 -> 23.8 where they leave no room to split K.  (With 128 x 128
+// blocks they load more for the same product: 33.2 -> 36.3 us for the first.)
+template <bool OUT_BF16>
+cudaError_t run_vec(const Fp8GemmArgs& g, cudaStream_t s) {
+    int64_t c192 = 0, c256 = 0;
+    cudaError_t e = run_split<192, false, true, OUT_BF16>(g, s, &c192);
+    if (e == cudaSuccess) e = run_split<256, false, true, OUT_BF16>(g, s, &c256);
+    if (e != cudaSuccess) return e;
+    return 8 * c192 <= 9 * c256 ? run_split<192, false, true, OUT_BF16>(g, s) : run_split<256, false, true, OUT_BF16>(g, s);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_fp8_split(const Fp8GemmArgs& g, cudaStream_t s) {
     if (g.M <= 16) return run_nt<16, true>(g, s);
     if (g.M <= 32) return run_nt<32, true>(g, s);
     if (g.M <= 64) return run_nt<64, true>(g, s);
-    return run_nt<256, false>(g, s);
+    if (g.b_lines == 1) return g.out_bf16 ? run_vec<true>(g, s) : run_vec<false>(g, s);
+    return g.out_bf16 ? run_split<256, false, false, true>(g, s) : run_split<256, false, false, false>(g, s);
 }
 
 }  // namespace fp4

@@ -129,7 +129,8 @@ def test_gemm_small(fp4, shape, b_lines, out_bf16):
 
 
 # outputs that run on CTA pairs: whole and ragged tiles, one chunk and many,
-# fewer tiles than pairs and several waves
+# fewer tiles than pairs and several waves (1 x 128 blocks: the first and third on
+# one round of 128 x 192 tiles)
 LARGE = [(1280, 2048, 256), (2300, 1900, 130), (1111, 2999, 1025), (2560, 2560, 100), (4096, 2300, 640)]
 
 
@@ -204,6 +205,13 @@ def test_quantizer_recovers_from_a_wait_that_runs_out(fp4, b_lines):
             assert torch.equal(a["codes"][:, :k], b["codes"][:, :k])
             m = n if b_lines == 1 else a["scales"].shape[1]
             assert torch.equal(a["scales"][:, :m], b["scales"][:, :m])
+
+
+@pytest.mark.parametrize("out_bf16", [False, True])
+@pytest.mark.parametrize("shape", [(1150, 4090, 256), (128, 14336, 512), (513, 6140, 300), (128, 4096, 2304)])
+def test_gemm_tiles_of_192_and_256_lines(fp4, shape, out_bf16):
+    """1 x 128 blocks on both widths, K whole and split: 256 for the first two."""
+    check_gemm(fp4, *shape, 1, out_bf16, seed=sum(shape))
 
 
 @pytest.mark.parametrize("M,N,out", [(3, 128 * 65536 + 40, "bf16"), (128 * 65536 + 40, 3, "f32")])
