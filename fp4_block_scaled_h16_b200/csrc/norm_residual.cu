@@ -344,7 +344,14 @@ norm_residual_kernel(const NormArgs a) {
                 for (int e = 0; e < PAIRS; ++e) m = fmaxf(m, fmaxf(fabsf(t[e].x), fabsf(t[e].y)));
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                const Fp8Block b = fp8_block(m, rstd);
+                float times = rstd;
+                if (m < 0x1p-100f) {         // 448 / m passes binary32: the codes of y itself
+#pragma unroll
+                    for (int e = 0; e < PAIRS; ++e) t[e] = __fmul2_rn(t[e], both(rstd));
+                    m = __fmul_rn(m, rstd);
+                    times = 1.0f;
+                }
+                const Fp8Block b = fp8_block(m, times);
                 if (live) {
                     const int i = tid + k * T;
                     if ((tid & 15) == 0) a.scales[(int64_t)(i >> 4) * a.lp + row] = b.s;

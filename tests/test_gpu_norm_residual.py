@@ -153,6 +153,24 @@ def test_norm_into_the_fp8_operand(fp4):
     assert (np.abs(quotient - middle) <= 84 * U * np.abs(quotient)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tiny", [2.0 ** -98, 2.0 ** -120, 2.0 ** -124])
+def test_blocks_of_tiny_values_in_the_fp8_operand(fp4, dtype, tiny):
+    """A block far below its row's RMS: y is a normal number, 448 over the block's
+    largest h' w is none.  A code is off by half a step, 2^-4 of it or 2^-10 of
+    the scale below the smallest normal one, and by the roundings of y and s."""
+    g = torch.Generator().manual_seed(9)
+    h = torch.randn((40, 512), generator=g) * 2.0 ** -14
+    h[:, 128:256] = torch.randn((40, 128), generator=g).clamp(0.25, 4) * tiny
+    h = h.to(dtype).cuda()
+    w = torch.ones(512, dtype=dtype, device="cuda")
+    q = fp4.norm_residual(h, w_pre=w, eps=0.0, quantize=True)["q"]
+    want = oracle.norm_residual(wide(h), w_pre=wide(w), eps=0.0)["y"]
+    scales = np.repeat(wide(q["scales"][:, :40].t()), 128, 1)
+    got = q["codes"].view(torch.float8_e4m3fn).double().cpu().numpy() * scales
+    assert_close(torch.from_numpy(got), want, 2.0 ** -4 * np.abs(want) * (1 + 2.0 ** -18) + 2.0 ** -10 * scales, "y")
+
+
 @pytest.mark.parametrize("rows,cols", [(3, 256), (1, 130)])
 def test_zero_rows_and_eps_zero(fp4, rows, cols):
     h = torch.zeros((rows, (cols + 7) // 8 * 8), device="cuda")[:, :cols]
