@@ -508,7 +508,8 @@ fp4_status_t fp4_fp8_block_quantize(const void* x, fp4_in_dtype_t in_dtype, int6
  *   c         device, [M, ldc] row-major, fp32 or bf16, ldc >= N
  * Shape rules: M, N and K may be anything >= 0 (K == 0 gives FP4_ERR_UNSUPPORTED_SHAPE
  * unless C is empty); code, scale and C pointers 16-byte aligned, ldc * size % 16 == 0.
- * Columns N .. ldc - 1 of C are left as they were.  The result does not depend
+ * Columns N .. ldc - 1 of C are left as they were.  The product of two scales
+ * that meet has to lie in the range of binary32.  The result does not depend
  * on timing.  A bounded wait that runs out is reported by fp4_last_error().
  */
 fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float* a_scales, const uint8_t* b_codes,

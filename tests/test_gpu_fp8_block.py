@@ -185,6 +185,21 @@ def test_gemm_wait_timeout_is_reported_and_recoverable(fp4, M, N, K, b_lines):
     assert torch.equal(before, after)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantizer_over_the_range_of_magnitudes(fp4, dtype):
+    """A block per power of two, the subnormal ones and the largest finite values among them."""
+    e = np.repeat(np.arange(-140, 128), 2)
+    rng = np.random.default_rng(11)
+    x = rng.uniform(0.5, 1.0, (len(e), 256)) * rng.choice([-1.0, 1.0], (len(e), 256))
+    x[:, 1::3] *= rng.uniform(0, 0.01, x[:, 1::3].shape)
+    x = torch.from_numpy((x * np.exp2(e.astype(np.float64))[:, None]).astype(np.float32)).to(dtype)
+    x[-1, :4] = torch.finfo(dtype).max
+    assert torch.isfinite(x).all()
+    o = oracle.fp8_block_quantize(oracle_input(x))
+    assert_same(fp4.fp8_block_quantize(x.cuda()), o, dtype == torch.bfloat16)
+    assert_same(fp4.fp8_block_quantize(x.t().contiguous().cuda(), 0), o, dtype == torch.bfloat16)
+
+
 @pytest.mark.parametrize("b_lines", [1, 128])
 def test_quantizer_recovers_from_a_wait_that_runs_out(fp4, b_lines):
     """One poll may or may not see the tile land; a call after it is right either way."""
