@@ -76,6 +76,33 @@ __device__ __forceinline__ Raw<BF16> load_raw(const void* p, int n) {
     return r;
 }
 
+// A vector of a row that is not its matrix's last, for 0 < n: the row's pitch is a
+// multiple of 16 bytes, so the words that hold its first n elements can be read
+// whole; what lies behind the row is cut off by clip() before use.  Loads under a
+// branch per vector kept the next row's from being in flight together: backward
+// 4771 x 8191 161 us, 8192 columns 77.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_words(const char* row, uint32_t off, int n) {
+    Raw<BF16> r;
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i)         // words without an element: the row's first, clipped
+        r.w[i] = *reinterpret_cast<const uint4*>(row + (n > 4 * i ? off + 16 * i : 0u));
+    return r;
+}
+
+// the vector with its elements from the n-th on as zeros
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> clip(Raw<BF16> r, int n) {
+    if (n >= VEC) return r;
+    uint32_t* const w = &r.w[0].x;
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+        const int left = BF16 ? n - 2 * i : 2 * (n - i);         // halves of the word that stay
+        w[i] = left >= 2 ? w[i] : (left == 1 ? w[i] & 0xffffu : 0u);
+    }
+    return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> zero_raw() {
     Raw<BF16> r;
@@ -245,6 +272,14 @@ norm_residual_kernel(const NormArgs a) {
     auto fetch = [&](int64_t row) {
         const char* h = row_at<BF16>(a.h, row * a.ldh);
         const char* o = row_at<BF16>(a.o, row * a.ldo);
+        if (!FULL && row + 1 < a.rows) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                hr[k] = load_words<BF16>(h, off[k], n[k]);
+                if (RES) orw[k] = load_words<BF16>(o, off[k], n[k]);
+            }
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             hr[k] = n[k] > 0 ? load_raw<BF16>(h + off[k], n[k]) : zero_raw<BF16>();
@@ -267,8 +302,8 @@ norm_residual_kernel(const NormArgs a) {
         float2 h[VPT][PAIRS], o[VPT][PAIRS];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            widen<BF16>(hr[k], h[k]);
-            if (RES) widen<BF16>(orw[k], o[k]);
+            widen<BF16>(FULL ? hr[k] : clip<BF16>(hr[k], n[k]), h[k]);
+            if (RES) widen<BF16>(FULL ? orw[k] : clip<BF16>(orw[k], n[k]), o[k]);
         }
         if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
         if (RES) {
@@ -359,10 +394,13 @@ norm_residual_kernel(const NormArgs a) {
                     uint8_t* dst = a.codes + row * a.ldc + VEC * i;
                     if (n[k] >= VEC) {
                         *reinterpret_cast<uint2*>(dst) = q;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VEC - 1; ++e)
-                            if (e < n[k]) dst[e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+                    } else {                 // 4, 2 and 1 codes
+                        const uint32_t b = n[k] & 4 ? q.y : q.x;
+                        if (n[k] & 4) *reinterpret_cast<uint32_t*>(dst) = q.x;
+                        dst += n[k] & 4;
+                        if (n[k] & 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)b;
+                        dst += n[k] & 2;
+                        if (n[k] & 1) *dst = (uint8_t)(b >> (n[k] & 2 ? 16 : 0));
                     }
                 }
             }
@@ -380,18 +418,22 @@ norm_residual_kernel(const NormArgs a) {
 // not depend on timing.  Columns past the row are zeros all the way and are only
 // left out of the stores.
 //
-// Four vectors per thread (beyond 8192 columns) do not fit the registers in this
-// form: there the row's inputs stay as they were loaded, without the next row's,
-// A, n1 and n2 are formed twice, and the sums are in shared memory.
+// Four vectors per thread (beyond 8192 columns), or two of fp32, do not fit the
+// registers in this form: there a row is read twice, the second time out of L2, to
+// which it comes while the row before is worked on, and the sums are in shared
+// memory (4096 x 4096 in fp32 91 us, 96 in registers with spills).  Rows beyond 8192
+// columns always take 512 threads, of which whole warps have fewer than four vectors.
 //
 // FULL as above.  PARTS: which parts of the operator are there, or -1 to ask the
 // arguments.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 constexpr int PART_PRE = 1, PART_RES = 2, PART_POST = 4;
 template <bool BF16, int VPT, int THREADS, bool FULL, int PARTS>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : (THREADS == 128 ? 4 : (VPT == 1 ? 3 : 2)))
 norm_residual_backward_kernel(const NormBwdArgs a) {
     constexpr uint32_t BYTES = VEC * (BF16 ? 2 : 4);
-    constexpr bool BIG = VPT == 4;
+    constexpr bool BIG = VPT == 4 || (VPT == 2 && !BF16);
     constexpr int KEPT = BIG ? 1 : VPT;       // vectors whose A, n1, n2 and sums stay in registers
     const bool pre = PARTS < 0 ? a.w_pre != nullptr : (PARTS & PART_PRE) != 0;
     const bool res = PARTS < 0 ? a.o != nullptr : (PARTS & PART_RES) != 0;
@@ -399,7 +441,7 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
     extern __shared__ float4 columns[];
     __shared__ float4 part[2][32];
     const int tid = (int)threadIdx.x, T = (int)blockDim.x, cols = (int)a.cols, vecs = T * VPT, warps = T >> 5;
-    // BIG: the second and third plane hold the sums of dw_pre and of the item
+    // BIG (see above): the second and third plane hold the sums of dw_pre and of the item
     const Columns factor{columns, vecs}, plane1{columns + 2 * vecs, vecs}, plane2{columns + 4 * vecs, vecs};
     const Columns w_pre = plane1, post = plane2, sum_pre = plane1, sum_item = plane2;
     const float inv_cols = 1.0f / (float)cols;
@@ -410,36 +452,61 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
         n[k] = FULL ? VEC : cols - VEC * (tid + k * T);
         off[k] = BYTES * (uint32_t)(tid + k * T);
     }
-    Raw<BF16> r_dhin[VPT], r_dy[VPT], r_h[VPT], r_o[VPT];
+    constexpr int SLOTS = BIG ? 2 : VPT;      // vectors as loaded; BIG: the next one while one is worked on
+    Raw<BF16> r_dhin[SLOTS], r_dy[SLOTS], r_h[SLOTS], r_o[SLOTS];
     float rstd2n = 0.0f, rstd1n = 1.0f;
-    auto fetch = [&](int64_t row) {
+    auto fetch_vector = [&](int64_t row, int k) {
+        const int j = k % SLOTS;
+        if (!FULL && row + 1 < a.rows) {
+            r_dhin[j] = a.dh_in ? load_words<BF16>(row_at<BF16>(a.dh_in, row * a.lddhi), off[k], n[k]) : zero_raw<BF16>();
+            if (pre) {
+                r_dy[j] = load_words<BF16>(row_at<BF16>(a.dy, row * a.lddy), off[k], n[k]);
+                r_h[j] = load_words<BF16>(row_at<BF16>(a.h, row * a.ldh), off[k], n[k]);
+            }
+            if (res) r_o[j] = load_words<BF16>(row_at<BF16>(a.o, row * a.ldo), off[k], n[k]);
+            return;
+        }
+        r_dhin[j] = a.dh_in ? load_raw<BF16>(row_at<BF16>(a.dh_in, row * a.lddhi) + off[k], n[k]) : zero_raw<BF16>();
+        if (pre) {
+            r_dy[j] = load_raw<BF16>(row_at<BF16>(a.dy, row * a.lddy) + off[k], n[k]);
+            r_h[j] = load_raw<BF16>(row_at<BF16>(a.h, row * a.ldh) + off[k], n[k]);
+        }
+        if (res) r_o[j] = load_raw<BF16>(row_at<BF16>(a.o, row * a.ldo) + off[k], n[k]);
+    };
+    auto fetch_rstd = [&](int64_t row) {
         if (pre) rstd2n = a.rstd_pre[row];
         if (has_post) rstd1n = a.rstd_post[row];
-        const char* dhin = row_at<BF16>(a.dh_in, row * a.lddhi);
-        const char* dy = row_at<BF16>(a.dy, row * a.lddy);
-        const char* h = row_at<BF16>(a.h, row * a.ldh);
-        const char* o = row_at<BF16>(a.o, row * a.ldo);
+    };
+    auto fetch = [&](int64_t row) {
+        fetch_rstd(row);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) fetch_vector(row, k);
+    };
+    // the row on its way to L2
+    auto ahead = [&](int64_t row, bool there) {
+        if (!there || (tid & (128 / (int)BYTES - 1))) return;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            r_dhin[k] = a.dh_in ? load_raw<BF16>(dhin + off[k], n[k]) : zero_raw<BF16>();
+            if (n[k] <= 0) continue;
+            if (a.dh_in) prefetch_l2(row_at<BF16>(a.dh_in, row * a.lddhi) + off[k]);
             if (pre) {
-                r_dy[k] = load_raw<BF16>(dy + off[k], n[k]);
-                r_h[k] = load_raw<BF16>(h + off[k], n[k]);
+                prefetch_l2(row_at<BF16>(a.dy, row * a.lddy) + off[k]);
+                prefetch_l2(row_at<BF16>(a.h, row * a.ldh) + off[k]);
             }
-            if (res) r_o[k] = load_raw<BF16>(o + off[k], n[k]);
+            if (res) prefetch_l2(row_at<BF16>(a.o, row * a.ldo) + off[k]);
         }
     };
     // A = dhin + rstd2 a, n2, n1 and d = a of vector k, from the row as loaded
     float rstd2 = 0.0f, rstd1 = 1.0f;
     auto form = [&](int k, float2 (&A)[PAIRS], float2 (&n2)[PAIRS], float2 (&n1)[PAIRS], float2 (&d)[PAIRS],
                     float2 (&dy)[PAIRS]) {
-        widen<BF16>(r_dhin[k], A);
+        widen<BF16>(FULL ? r_dhin[k % SLOTS] : clip<BF16>(r_dhin[k % SLOTS], n[k]), A);
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) n2[e] = n1[e] = d[e] = dy[e] = both(0.0f);
-        if (res) widen<BF16>(r_o[k], n1);
+        if (res) widen<BF16>(FULL ? r_o[k % SLOTS] : clip<BF16>(r_o[k % SLOTS], n[k]), n1);
         if (pre) {
-            widen<BF16>(r_h[k], n2);
-            widen<BF16>(r_dy[k], dy);
+            widen<BF16>(FULL ? r_h[k % SLOTS] : clip<BF16>(r_h[k % SLOTS], n[k]), n2);
+            widen<BF16>(FULL ? r_dy[k % SLOTS] : clip<BF16>(r_dy[k % SLOTS], n[k]), dy);
             if (BIG) widen<BF16>(load_raw<BF16>(row_at<BF16>(a.w_pre, 0) + off[k], n[k]), d);
             else w_pre.get(tid + k * T, d);
 #pragma unroll
@@ -501,12 +568,16 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
                 if (!BIG) acc[BIG ? 0 : k][e] = f[e];
             }
             if (BIG) sum_item.set(tid + k * T, f);
-            if (!res) continue;
+            if (!res || (BIG && n[k] <= 0)) continue;
             branch_factor<BF16>(has_post ? a.w_post : nullptr, a.gate, a.ldg, a.alpha, grp, off[k], n[k], f);
             factor.set(tid + k * T, f);
         }
         for (; row < last; ++row) {
-            if (BIG) fetch(row);
+            if (BIG) {
+                fetch_rstd(row);
+                fetch_vector(row, 0);
+                ahead(row + 1 < last ? row + 1 : row_next, row + 1 < last || row_next < last_next);
+            }
             rstd2 = rstd2n;
             rstd1 = rstd1n;
             // with dh' = A - rstd2 n2 c1, both means follow from three sums of one
@@ -517,6 +588,8 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int i = tid + k * T, j = BIG ? 0 : k;
+                if (BIG && k + 1 < VPT) fetch_vector(row, k + 1);
+                if (BIG && n[k] <= 0) continue;
                 float2 d[PAIRS], dy[PAIRS];
                 form(k, A[j], n2[j], n1[j], d, dy);
                 if (pre) {
@@ -541,7 +614,9 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
                     }
                 }
             }
-            if (!BIG) {
+            if (BIG) {
+                fetch_vector(row, 0);
+            } else {
                 if (row + 1 < last) fetch(row + 1);
                 else if (row_next < last_next) fetch(row_next);
             }
@@ -558,6 +633,8 @@ norm_residual_backward_kernel(const NormBwdArgs a) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int i = tid + k * T, j = BIG ? 0 : k;
+                if (BIG && k + 1 < VPT) fetch_vector(row, k + 1);
+                if (BIG && n[k] <= 0) continue;
                 if (BIG) {
                     float2 d[PAIRS], dy[PAIRS];
                     form(k, A[j], n2[j], n1[j], d, dy);
@@ -791,7 +868,7 @@ cudaError_t launch_columns(const Args& a, cudaStream_t s) {
     if constexpr (std::is_same<Args, NormBwdArgs>::value)
         if (threads <= 128) return launch_shape<BF16, 1, 128>(a, threads, s);
     if (vpt == 1) return launch_shape<BF16, 1, 256>(a, threads, s);
-    if (vpt == 4) return launch_shape<BF16, 4, 512>(a, threads, s);
+    if (vpt == 4) return launch_shape<BF16, 4, 512>(a, std::is_same<Args, NormBwdArgs>::value ? 512 : threads, s);
     return threads <= 256 ? launch_shape<BF16, 2, 256>(a, threads, s) : launch_shape<BF16, 2, 512>(a, threads, s);
 }
 
@@ -800,9 +877,20 @@ cudaError_t launch_columns(const Args& a, cudaStream_t s) {
 void norm_bwd_plan(NormBwdArgs& a) {
     a.groups = a.gate ? (a.rows + a.per - 1) / a.per : 1;
     if (!a.gate) a.per = a.rows;
-    // segments per group: enough items for every CTA, each of at least one row
-    int64_t nseg = (norm_bwd_limit(a.cols) + a.groups - 1) / a.groups;
-    if (nseg > a.per) nseg = a.per;
+    // segments per group: as many as fill one to four rounds of the CTAs, whichever
+    // leaves the busiest CTA the fewest rows, an item's own time counted as two
+    const int64_t limit = norm_bwd_limit(a.cols);
+    int64_t nseg = 1, best = (a.groups + limit - 1) / limit * (a.per + 2);
+    for (int64_t k = 1; k <= 4; ++k) {
+        int64_t n = k * limit / a.groups;
+        if (n > a.per) n = a.per;
+        if (n <= nseg) continue;
+        const int64_t cost = (n * a.groups + limit - 1) / limit * ((a.per + n - 1) / n + 2);
+        if (cost < best) {
+            best = cost;
+            nseg = n;
+        }
+    }
     a.seg_rows = (a.per + nseg - 1) / nseg;
     a.nseg = (a.per + a.seg_rows - 1) / a.seg_rows;
     a.items = a.groups * a.nseg;

@@ -238,6 +238,31 @@ def test_gradients_do_not_depend_on_timing(fp4):
         assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(5, 1), (40, 131), (33, 1003), (20, 2035), (9, 5501), (7, 8501)])
+def test_what_lies_behind_a_row_is_not_seen(fp4, rows, cols, dtype):
+    """NaN up to the row's pitch, and no bytes at all behind the last row."""
+    def holed(t, fill):
+        ld = (cols + 7) // 8 * 8 + 8
+        flat = torch.full(((t.shape[0] - 1) * ld + cols,), fill, dtype=dtype, device="cuda")
+        v = flat.as_strided(t.shape, (ld, 1))
+        v.copy_(t)
+        return v
+    a = inputs(rows, cols, dtype, True, 4, 0, 31)
+    g = torch.Generator().manual_seed(32)
+    dy, dh_in = matrix(g, rows, cols, dtype), matrix(g, rows, cols, dtype)
+    got = []
+    for fill in (0.0, float("nan")):
+        b = {k: holed(v, fill) if v.dim() == 2 else v for k, v in a.items()}
+        f = fp4.norm_residual(alpha=0.5, rows_per_group=4, quantize=True, out=dict(y=holed(dy, fill)), **b)
+        r = fp4.norm_residual_backward(holed(dy, fill), holed(f["h"], fill), f["rstd_pre"], w_pre=b["w_pre"],
+                                       dh_in=holed(dh_in, fill), o=b["o"], w_post=b["w_post"],
+                                       rstd_post=f["rstd_post"], gate=b["gate"], rows_per_group=4, alpha=0.5)
+        got.append(dict(h=f["h"], y=f["y"], codes=f["q"]["codes"][:, :cols], scales=f["q"]["scales"][:, :rows], **r))
+    for k, v in got[0].items():
+        assert torch.isfinite(v.float()).all() and torch.equal(v, got[1][k]), k
+
+
 def test_own_workspace_on_another_stream(fp4, monkeypatch):
     """The workspace that the helper allocates is not handed out again before the
     call has run on its stream."""
