@@ -26,8 +26,9 @@
 // rounded before its norm, because the stored h' is what the next block and the
 // backward call see.
 //
-// 8192 x 4096 in bf16, both weights and a gate: forward 49.2 us (5460 GB/s), with
-// FP8 codes for y 41 us (5800 GB/s), backward with its sums 75 us (5370 GB/s).  What
+// 8192 x 4096 in bf16, both weights and a gate: forward 48 us (5600 GB/s; 44 us
+// without a gate), backward with its sums 75 us (5370 GB/s); without w_post, FP8
+// codes for y, 42 us (5650 GB/s).  What
 // is left to the copy rate is the block sums' barrier between a row's loads and its
 // stores, and in the backward call the arithmetic of the three sums.  One row 3.3
 // us; a backward call adds a second launch, 6 us at least.
@@ -288,7 +289,13 @@ norm_residual_kernel(const NormArgs a) {
     };
     int64_t grp = -1;
     int turn = 0;
-    if ((int64_t)blockIdx.x < a.rows) fetch(blockIdx.x);
+    // Neighbouring CTAs take neighbouring rows (8192 x 4096 43.9 us, 47.1 with a run
+    // of rows per CTA), but with a gate a run per CTA, so that the gate row seldom
+    // changes (3589 x 5348 in groups of 156 rows 63 us, 103 the other way).
+    const int64_t step = a.gate ? 1 : gridDim.x;
+    const int64_t row_end = a.gate ? a.rows * (blockIdx.x + 1) / gridDim.x : a.rows;
+    int64_t row = a.gate ? a.rows * blockIdx.x / gridDim.x : blockIdx.x;
+    if (row < row_end) fetch(row);
     if (a.w_pre) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -298,14 +305,14 @@ norm_residual_kernel(const NormArgs a) {
             w_pre.set(tid + k * T, v);
         }
     }
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (; row < row_end; row += step) {
         float2 h[VPT][PAIRS], o[VPT][PAIRS];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             widen<BF16>(FULL ? hr[k] : clip<BF16>(hr[k], n[k]), h[k]);
             if (RES) widen<BF16>(FULL ? orw[k] : clip<BF16>(orw[k], n[k]), o[k]);
         }
-        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        if (row + step < row_end) fetch(row + step);
         if (RES) {
             const int64_t g = a.gate ? row / a.per : 0;
             if (g != grp) {
@@ -777,7 +784,7 @@ void shape_of(int64_t cols, int& vpt, int& threads) {
 
 // CTAs of the backward kernel, which have a line of partial sums each: as many as a
 // B200 holds at once, three per SM with up to 256 threads of one vector, two with
-// two, one beyond 4096 columns (4364 x 2034 47 us, 57 with two per SM).  Rows of up
+// two, one beyond 4096 columns (4364 x 2034 47 us at the time, 57 with two).  Rows of up
 // to 1024 columns have a form of 128 threads with all their registers and take 512
 // threads per SM: with 768 the longer sum over the lines costs more than the rows
 // gain (1031 x 1003 12.2 us against 14.1).
