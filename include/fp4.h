@@ -538,7 +538,8 @@ fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float
  *   codes, ld_codes, scales   or NULL
  *   rstd_post, rstd_pre   float [rows], written where the norm is taken
  * Shape rules: cols <= 16384, rows < 2^31 - 512; every matrix pointer 16-byte
- * aligned with a pitch that is a multiple of 16 bytes.  w_pre needs y or codes (and
+ * aligned with a pitch that is a multiple of 16 bytes (what lies between a row's
+ * end and its pitch may be read but is not used; behind the last row, not even read).  w_pre needs y or codes (and
  * they need w_pre); w_post and gate need o; eps >= 0 and finite, alpha finite.
  * A row whose sum of squares passes the range of binary32, a row of zeros with
  * eps 0 and a row with non-finite elements have unspecified results; they do not
