@@ -6,7 +6,7 @@
 //
 // An FP32 scale per 128-K chunk cannot ride in the tensor core's accumulator,
 // so every chunk is a partial product of its own, promoted in binary32
-// registers: acc += sA (sB P).  The partial of a chunk is 256 x 256 over a CTA
+// registers: acc += (sA sB) P.  The partial of a chunk is 256 x 256 over a CTA
 // pair (tcgen05.mma cta_group::2 kind::f8f6f4, four of K = 32), 128 x 256 per
 // CTA: 256 TMEM columns, so all 512 columns hold two partials and the tensor
 // core fills one while eight warps promote the other.
@@ -59,7 +59,7 @@ constexpr int MMA_WARPS = 2;
 constexpr int PROMO_WARPS = 8;
 constexpr int NUM_THREADS = 128 + 32 * PROMO_WARPS;
 // registers per thread: at launch, of warps 0-3, and of the promotion warps
-constexpr int REGS_LAUNCH = 168, REGS_LEAD = 64, REGS_PROMO = 216;
+constexpr int REGS_LAUNCH = 168, REGS_LEAD = 56, REGS_PROMO = 224;
 static_assert(128 * REGS_LEAD + 32 * PROMO_WARPS * REGS_PROMO <= NUM_THREADS * REGS_LAUNCH, "register split");
 constexpr int COLS = PN / (PROMO_WARPS / 4);         // columns of the tile per promotion warp
 constexpr int STAGES = 5;
@@ -303,8 +303,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 // the chunk's scales landed before its MMAs ran
                 const float* sc = reinterpret_cast<const float*>(sc_ring + slot * SC_BYTES);
                 const float sa = sc[32 * q + lane];
-                const float s = VEC ? sa : __fmul_rn(sa, sb);
-                const float2 s2 = make_float2(s, s);
+                float s = VEC ? sa : __fmul_rn(sa, sb);
                 const float4* sbv = reinterpret_cast<const float4*>(sc + 128 + cg * COLS);
                 // 64 columns in flight at a time
 #pragma unroll
@@ -323,18 +322,22 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         if (pb == 0) pphase ^= 1u;
                         seen = sm100::mbar_test_wait(&pfull[pb], pphase);    // the next chunk's, ahead of the sums
                     }
+                    const float2 s2 = make_float2(s, s);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const uint32_t* v = &r[c >> 3][4 * (c & 7)];
-                        float2 p0 = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                        float2 p1 = make_float2(__uint_as_float(v[2]), __uint_as_float(v[3]));
+                        // the scales' product first: it lies in the range of binary32,
+                        // a partial times one of them need not
+                        float2 w0 = s2, w1 = s2;
                         if (VEC) {
                             const float4 w = sbv[16 * g + c];
-                            p0 = __fmul2_rn(p0, make_float2(w.x, w.y));
-                            p1 = __fmul2_rn(p1, make_float2(w.z, w.w));
+                            w0 = __fmul2_rn(make_float2(w.x, w.y), s2);
+                            w1 = __fmul2_rn(make_float2(w.z, w.w), s2);
                         }
-                        acc[32 * g + 2 * c] = __ffma2_rn(p0, s2, acc[32 * g + 2 * c]);
-                        acc[32 * g + 2 * c + 1] = __ffma2_rn(p1, s2, acc[32 * g + 2 * c + 1]);
+                        acc[32 * g + 2 * c] = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), w0,
+                                                         acc[32 * g + 2 * c]);
+                        acc[32 * g + 2 * c + 1] = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                                                             w1, acc[32 * g + 2 * c + 1]);
                     }
                 }
                 if (++slot == SC_SLOTS) slot = 0;

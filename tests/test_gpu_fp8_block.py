@@ -260,3 +260,28 @@ def test_two_streams_at_once(fp4):
         outs.append(fp4.fp8_block_gemm(qa, qb, stream=s))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+# outputs of the pair kernel and of the split kernel's 16-, 64-, 192- and 256-line tiles
+@pytest.mark.parametrize("M,N,K", [(4096, 2300, 200), (2300, 1900, 130), (1150, 4090, 256), (130, 300, 200), (40, 300, 260),
+                                   (3, 200, 130)])
+@pytest.mark.parametrize("b_lines", [1, 128])
+@pytest.mark.parametrize("ea,eb", [(-110, 124), (118, -105)])
+def test_gemm_with_scales_far_apart(fp4, M, N, K, b_lines, ea, eb):
+    """The product of two scales lies near 1, but a partial product times one of them passes binary32."""
+    rng = np.random.default_rng(M + N)
+    a = (rng.standard_normal((M, K)) * 2.0 ** ea).astype(np.float32)
+    b = (rng.standard_normal((N, K)) * 0.05 * 2.0 ** eb).astype(np.float32)
+    oa, ob = oracle.fp8_block_quantize(a, 1), oracle.fp8_block_quantize(b, b_lines)
+    assert np.isfinite(a).all() and np.isfinite(b).all()
+    assert max(oa["scales"].max(), ob["scales"].max()) > 2.0 ** 108 and max(oa["scales"].min(), ob["scales"].min()) > 1
+    C64, bound = oracle.fp8_block_gemm(oa, ob)
+    for pairs in (True, False):
+        fp4.fp4_set_gemm_cta_pairs(pairs)
+        try:
+            C = fp4.fp8_block_gemm(upload(fp4, oa), upload(fp4, ob))
+        finally:
+            fp4.fp4_set_gemm_cta_pairs(True)
+        assert torch.isfinite(C).all()
+        assert_within_gemm_bound(C.cpu().numpy(), C64, bound, False, "%s" % ((M, N, K, b_lines, ea, eb, pairs),))
+    assert fp4.fp4_last_error() == fp4.FP4_OK
