@@ -365,33 +365,44 @@ norm_residual_kernel(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const bool live = n[k] > 0;
-            // y = RN(RN(h' w) rstd): for bf16 the first product is exact
-            float2 t[PAIRS], f[PAIRS];
+            float2 f[PAIRS];
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) f[e] = both(0.0f);
             if (live) w_pre.get(tid + k * T, f);
+            // y = RN(RN(h' rstd) w): h' rstd lies near 1, where h' w may pass binary32
+            // although y does not
+            auto product = [&](float2 (&y)[PAIRS]) {
 #pragma unroll
-            for (int e = 0; e < PAIRS; ++e) t[e] = __fmul2_rn(h[k][e], f[e]);
+                for (int e = 0; e < PAIRS; ++e) y[e] = __fmul2_rn(__fmul2_rn(h[k][e], both(rstd)), f[e]);
+            };
             if (a.y && live) {
                 float2 y[PAIRS];
-#pragma unroll
-                for (int e = 0; e < PAIRS; ++e) y[e] = __fmul2_rn(t[e], both(rstd));
+                product(y);
                 store_raw<BF16>(y_out + off[k], n[k], narrow<BF16>(y));
             }
             if (a.codes) {
                 // a block of 128 columns is 16 lanes' vectors; its codes follow from
-                // h' w alone, because rstd is common to the block
-                float m = 0.0f;
+                // h' w alone, because rstd is common to the block (for bf16 exact, so
+                // that ties of y stay ties)
+                auto block_max = [&](const float2 (&v)[PAIRS]) {
+                    float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < PAIRS; ++e) m = fmaxf(m, fmaxf(fabsf(t[e].x), fabsf(t[e].y)));
+                    for (int e = 0; e < PAIRS; ++e) m = fmaxf(m, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
 #pragma unroll
-                for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                float times = rstd;
-                if (m < 0x1p-100f) {         // 448 / m passes binary32: the codes of y itself
+                    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    return m;
+                };
+                float2 t[PAIRS];
 #pragma unroll
-                    for (int e = 0; e < PAIRS; ++e) t[e] = __fmul2_rn(t[e], both(rstd));
-                    m = __fmul_rn(m, rstd);
-                    times = 1.0f;
+                for (int e = 0; e < PAIRS; ++e) t[e] = __fmul2_rn(h[k][e], f[e]);
+                float m = block_max(t), times = rstd;
+                const bool far = !(m >= 0x1p-100f && m <= 0x1p100f);
+                if (__any_sync(0xffffffffu, far)) {     // 448 / m or h' w pass binary32: the codes of y itself
+                    if (far) {
+                        product(t);
+                        times = 1.0f;
+                    }
+                    m = block_max(t);
                 }
                 const Fp8Block b = fp8_block(m, times);
                 if (live) {

@@ -541,6 +541,7 @@ fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float
  * aligned with a pitch that is a multiple of 16 bytes (what lies between a row's
  * end and its pitch may be read but is not used; behind the last row, not even read).  w_pre needs y or codes (and
  * they need w_pre); w_post and gate need o; eps >= 0 and finite, alpha finite.
+ * alpha gate w_post, column by column, has to lie in the range of binary32.
  * A row whose sum of squares passes the range of binary32, a row of zeros with
  * eps 0 and a row with non-finite elements have unspecified results; they do not
  * reach other rows.

@@ -292,3 +292,20 @@ def test_own_workspace_on_another_stream(fp4, monkeypatch):
         torch.cuda.synchronize()
         for k in want:
             assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eh,ew", [(50, 80), (-40, -90)])
+def test_stream_and_weight_far_from_one(fp4, dtype, eh, ew):
+    """h' w passes binary32 at one end, while y does not."""
+    rows, cols = 21, 1000
+    g = torch.Generator().manual_seed(eh - ew)
+    h = (torch.randn((rows, cols), generator=g) * 2.0 ** eh).to(dtype).cuda()
+    w = ((1 + 0.2 * torch.randn(cols, generator=g)) * 2.0 ** ew).to(dtype).cuda()
+    f = fp4.norm_residual(h, w_pre=w, eps=0.0, quantize=True, out=dict(y=torch.empty_like(h)))
+    want = oracle.norm_residual(wide(h), w_pre=wide(w), eps=0.0)["y"]
+    half = half_step(dtype)
+    assert_close(f["y"], want, (40 * U + half) * np.abs(want), "y")
+    scales = np.repeat(wide(f["q"]["scales"][:, :rows].t()), 128, 1)[:, :cols]
+    got = f["q"]["codes"][:, :cols].view(torch.float8_e4m3fn).double().cpu().numpy() * scales
+    assert_close(torch.from_numpy(got), want, 2.0 ** -4 * np.abs(want) * (1 + 2.0 ** -18) + 2.0 ** -10 * scales, "codes")
