@@ -309,3 +309,84 @@ def test_stream_and_weight_far_from_one(fp4, dtype, eh, ew):
     scales = np.repeat(wide(f["q"]["scales"][:, :rows].t()), 128, 1)[:, :cols]
     got = f["q"]["codes"][:, :cols].view(torch.float8_e4m3fn).double().cpu().numpy() * scales
     assert_close(torch.from_numpy(got), want, 2.0 ** -4 * np.abs(want) * (1 + 2.0 ** -18) + 2.0 ** -10 * scales, "codes")
+
+
+# Many rows per CTA, and more groups than CTAs.  A CTA sums at most 14 rows here, a
+# column at most 2368 CTAs' partial sums, every 32nd of them (74) and then 32 such:
+# with the product's 6 roundings 126, under 140 u for dw_pre and, with the 140 of
+# the terms themselves, 280 u for dw_post and dgate.
+LOOPS = [(3000, 2056, 0), (3000, 2056, 1), (3000, 2056, 7), (3000, 2056, 2000), (900, 4104, 1), (900, 4104, 3),
+         (700, 8200, 1), (700, 8200, 3), (5000, 130, 0), (5000, 130, 1), (5000, 130, 7), (1500, 4096, 700)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols,per", LOOPS)
+def test_many_rows_and_groups_per_cta(fp4, dtype, rows, cols, per):
+    alpha, eps = 0.75, 1e-5
+    t = inputs(rows, cols, dtype, True, per, pad=16, seed=rows + cols + per)
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"], o=t["o"], w_post=t["w_post"], gate=t["gate"],
+                          rows_per_group=per or None, alpha=alpha, eps=eps)
+    w = {k: wide(v) for k, v in t.items()}
+    ref = oracle.norm_residual(w["h"], w["o"], w["w_post"], w["gate"], per, alpha, None, eps)
+    size = np.abs(w["h"]) + np.abs(ref["h"] - w["h"])
+    half = half_step(dtype)
+    assert_close(f["h"], ref["h"], 40 * U * size + half * np.abs(ref["h"]) * (1 + 40 * U), "h'")
+    kept = wide(f["h"])
+    ref2 = oracle.norm_residual(kept, w_pre=w["w_pre"], eps=eps)
+    assert_close(f["y"], ref2["y"], (40 * U + half) * np.abs(ref2["y"]), "y")
+    g = torch.Generator().manual_seed(cols)
+    dy, dh_in = (matrix(g, rows, cols, dtype, 16) for _ in range(2))
+    want_in = wide(dh_in)
+    # in place: dh takes dh_in's memory
+    b = fp4.norm_residual_backward(dy, f["h"], f["rstd_pre"], w_pre=t["w_pre"], dh_in=dh_in, o=t["o"],
+                                   w_post=t["w_post"], rstd_post=f["rstd_post"], gate=t["gate"],
+                                   rows_per_group=per or None, alpha=alpha, out=dict(dh=dh_in))
+    r = oracle.norm_residual_backward(wide(dy), kept, wide(f["rstd_pre"]), w["w_pre"], want_in, w["o"],
+                                      w["w_post"], wide(f["rstd_post"]), w["gate"], per, alpha)
+    for name, count in (("dh", 70), ("do", 140), ("dw_pre", 140), ("dw_post", 280), ("dgate", 280)):
+        if r[name] is None:
+            assert b[name] is None
+            continue
+        tol = count * U * r["size"][name] + (half * np.abs(r[name]) if name in ("dh", "do") else 0.0)
+        assert_close(b[name], r[name], tol, name)
+    assert fp4.fp4_last_error() == fp4.FP4_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [2056, 4096, 8192, 12288])
+def test_parts_of_the_operator_at_model_widths(fp4, dtype, cols):
+    """Each half alone, and the update with its norm but none after it; up to 5 rows per CTA."""
+    rows, per = 700, 9
+    t = inputs(rows, cols, dtype, True, per, 0, cols)
+    w = {k: wide(v) for k, v in t.items()}
+    half = half_step(dtype)
+    g = torch.Generator().manual_seed(cols + 1)
+    dy, dh_in = (matrix(g, rows, cols, dtype) for _ in range(2))
+
+    def check(b, r):
+        for name, count in (("dh", 70), ("do", 140), ("dw_pre", 140), ("dw_post", 280), ("dgate", 280)):
+            assert (b[name] is None) == (r[name] is None), name
+            if r[name] is not None:
+                tol = count * U * r["size"][name] + (half * np.abs(r[name]) if name in ("dh", "do") else 0.0)
+                assert_close(b[name], r[name], tol, name)
+
+    # the norm alone, and its gradients with and without what reaches the stream besides
+    f = fp4.norm_residual(t["h"], w_pre=t["w_pre"])
+    ref = oracle.norm_residual(w["h"], w_pre=w["w_pre"])
+    assert_close(f["y"], ref["y"], (40 * U + half) * np.abs(ref["y"]), "y")
+    for extra in (None, dh_in):
+        check(fp4.norm_residual_backward(dy, t["h"], f["rstd_pre"], w_pre=t["w_pre"], dh_in=extra),
+              oracle.norm_residual_backward(wide(dy), w["h"], wide(f["rstd_pre"]), w["w_pre"], wide(extra), None, None,
+                                            None, None, 0, 1))
+    # the update alone: without its norm, with it, and with a gate
+    for post, gated in ((False, False), (True, False), (False, True), (True, True)):
+        kw = dict(w_post=t["w_post"] if post else None, gate=t["gate"] if gated else None,
+                  rows_per_group=per if gated else None, alpha=-2.0)
+        f = fp4.norm_residual(t["h"], o=t["o"], **kw)
+        wp, wg = w["w_post"] if post else None, w["gate"] if gated else None
+        ref = oracle.norm_residual(w["h"], w["o"], wp, wg, per, -2.0, None, 1e-6)
+        size = np.abs(w["h"]) + np.abs(ref["h"] - w["h"])
+        assert_close(f["h"], ref["h"], 40 * U * size + half * np.abs(ref["h"]) * (1 + 40 * U), "h'")
+        check(fp4.norm_residual_backward(None, None, dh_in=dh_in, o=t["o"], rstd_post=f["rstd_post"], **kw),
+              oracle.norm_residual_backward(None, None, None, None, wide(dh_in), w["o"], wp, wide(f["rstd_post"]), wg,
+                                            per, -2.0))
