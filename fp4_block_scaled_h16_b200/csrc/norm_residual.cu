@@ -47,6 +47,7 @@ namespace {
 
 constexpr int VEC = 8;                   // elements per vector
 constexpr int PAIRS = VEC / 2;
+constexpr float TINY_EPS = 0x1p-96f;
 
 // a vector as it is in memory: one (bf16) or two (fp32) 16-byte words
 template <bool BF16>
@@ -248,13 +249,41 @@ __device__ __forceinline__ float block_sum(float v, float* part, int tid, int wa
     return s;
 }
 
-__device__ __forceinline__ float rstd_of(float sum, float cols, float eps) {
-    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, cols), eps)));
+// 1 / sqrt(mean + eps) over a row that the CTA holds in registers.  TINY: where that
+// mean lies so low that squares were lost to binary32's lower end, they are summed
+// again from values times 2^96, whose squares are normal numbers.
+template <bool TINY, int VPT>
+__device__ __forceinline__ float rstd_of(const float2 (&v)[VPT][PAIRS], float cols, float eps, float (&part)[2][32],
+                                         int& turn, int tid, int warps) {
+    float2 s2 = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(v[k][e], v[k][e], s2);
+    float m = __fadd_rn(__fdiv_rn(block_sum(s2.x + s2.y, part[turn], tid, warps), cols), eps);
+    turn ^= 1;
+    if (TINY && m < TINY_EPS) {              // the same in every thread
+        s2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) {
+                const float2 x = __fmul2_rn(v[k][e], both(0x1p96f));
+                s2 = __ffma2_rn(x, x, s2);
+            }
+        m = __fadd_rn(__fdiv_rn(block_sum(s2.x + s2.y, part[turn], tid, warps), cols), eps * 0x1p96f * 0x1p96f);
+        turn ^= 1;
+        return __frcp_rn(__fsqrt_rn(m)) * 0x1p96f;
+    }
+    return __frcp_rn(__fsqrt_rn(m));
 }
 
 // FULL: the row is exactly the CTA's vectors, none of them partial or empty.
-// POST: the block output is normalised; RES: there is one.
-template <bool BF16, int VPT, int THREADS, bool FULL, bool RES, bool POST>
+// POST: the block output is normalised; RES: there is one.  TINY: eps lies below
+// TINY_EPS, so that a row's mean square may, too.  Any other eps keeps mean + eps
+// above it, and takes forms without the second sum, whose registers spill (fp32
+// 4096 x 4096 54 us, 67 with it).
+template <bool BF16, int VPT, int THREADS, bool FULL, bool RES, bool POST, bool TINY>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : (VPT == 1 ? 4 : 3))
 norm_residual_kernel(const NormArgs a) {
     constexpr uint32_t BYTES = VEC * (BF16 ? 2 : 4);
@@ -327,13 +356,7 @@ norm_residual_kernel(const NormArgs a) {
             }
             float rstd = 1.0f;
             if (POST) {
-                float2 s2 = both(0.0f);
-#pragma unroll
-                for (int k = 0; k < VPT; ++k)
-#pragma unroll
-                    for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(o[k][e], o[k][e], s2);
-                rstd = rstd_of(block_sum(s2.x + s2.y, part[turn], tid, warps), (float)cols, a.eps);
-                turn ^= 1;
+                rstd = rstd_of<TINY>(o, (float)cols, a.eps, part, turn, tid, warps);
                 if (tid == 0) a.rstd_post[row] = rstd;
             }
             char* h_out = row_at<BF16>(a.h_out, row * a.ldho);
@@ -353,13 +376,7 @@ norm_residual_kernel(const NormArgs a) {
             }
         }
         if (!a.w_pre) continue;
-        float2 s2 = both(0.0f);
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int e = 0; e < PAIRS; ++e) s2 = __ffma2_rn(h[k][e], h[k][e], s2);
-        const float rstd = rstd_of(block_sum(s2.x + s2.y, part[turn], tid, warps), (float)cols, a.eps);
-        turn ^= 1;
+        const float rstd = rstd_of<TINY>(h, (float)cols, a.eps, part, turn, tid, warps);
         if (tid == 0) a.rstd_pre[row] = rstd;
         char* y_out = row_at<BF16>(a.y, row * a.ldy);
 #pragma unroll
@@ -810,11 +827,11 @@ int64_t norm_bwd_ctas(const NormBwdArgs& a) {
     return a.items < limit ? a.items : limit;
 }
 
-template <bool BF16, int VPT, int THREADS, bool FULL, bool RES, bool POST>
+template <bool BF16, int VPT, int THREADS, bool FULL, bool TINY, bool RES, bool POST>
 cudaError_t run_norm(const NormArgs& a, int threads, cudaStream_t s) {
     static PerDeviceOnce setup;
     static int per_sm[kOnceDevices][17] = {};
-    constexpr auto kernel = norm_residual_kernel<BF16, VPT, THREADS, FULL, RES, POST>;
+    constexpr auto kernel = norm_residual_kernel<BF16, VPT, THREADS, FULL, RES, POST, TINY>;
     const auto smem = [](int t) { return (size_t)t * VPT * VEC * sizeof(float) * (RES ? 2 : 1); };
     int dev = 0;
     const cudaError_t e = setup.run([&](int d) {
@@ -833,11 +850,11 @@ cudaError_t run_norm(const NormArgs& a, int threads, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <bool BF16, int VPT, int THREADS, bool FULL>
+template <bool BF16, int VPT, int THREADS, bool FULL, bool TINY>
 cudaError_t run_norm_parts(const NormArgs& a, int threads, cudaStream_t s) {
-    if (!a.o) return run_norm<BF16, VPT, THREADS, FULL, false, false>(a, threads, s);
-    return a.w_post ? run_norm<BF16, VPT, THREADS, FULL, true, true>(a, threads, s)
-                    : run_norm<BF16, VPT, THREADS, FULL, true, false>(a, threads, s);
+    if (!a.o) return run_norm<BF16, VPT, THREADS, FULL, TINY, false, false>(a, threads, s);
+    return a.w_post ? run_norm<BF16, VPT, THREADS, FULL, TINY, true, true>(a, threads, s)
+                    : run_norm<BF16, VPT, THREADS, FULL, TINY, true, false>(a, threads, s);
 }
 
 template <bool BF16, int VPT, int THREADS, bool FULL, int PARTS>
@@ -870,8 +887,9 @@ cudaError_t run_norm_bwd_parts(const NormBwdArgs& a, int threads, cudaStream_t s
 
 template <bool BF16, int VPT, int THREADS>
 cudaError_t launch_shape(const NormArgs& a, int threads, cudaStream_t s) {
-    return a.cols == (int64_t)threads * VPT * VEC ? run_norm_parts<BF16, VPT, THREADS, true>(a, threads, s)
-                                                  : run_norm_parts<BF16, VPT, THREADS, false>(a, threads, s);
+    if (a.eps < TINY_EPS) return run_norm_parts<BF16, VPT, THREADS, false, true>(a, threads, s);
+    return a.cols == (int64_t)threads * VPT * VEC ? run_norm_parts<BF16, VPT, THREADS, true, false>(a, threads, s)
+                                                  : run_norm_parts<BF16, VPT, THREADS, false, false>(a, threads, s);
 }
 template <bool BF16, int VPT, int THREADS>
 cudaError_t launch_shape(const NormBwdArgs& a, int threads, cudaStream_t s) {

@@ -542,9 +542,9 @@ fp4_status_t fp4_fp8_block_gemm(const uint8_t* a_codes, int64_t lda, const float
  * end and its pitch may be read but is not used; behind the last row, not even read).  w_pre needs y or codes (and
  * they need w_pre); w_post and gate need o; eps >= 0 and finite, alpha finite.
  * alpha gate w_post, column by column, has to lie in the range of binary32.
- * A row whose sum of squares passes the range of binary32, a row of zeros with
- * eps 0 and a row with non-finite elements have unspecified results; they do not
- * reach other rows.
+ * A row whose sum of squares passes the range of binary32, with eps 0 a row whose
+ * rstd does (zeros, or an RMS below 2^-127), and a row with
+ * non-finite elements have unspecified results; they do not reach other rows.
  */
 fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_t ldh, fp4_in_dtype_t dtype,
                                int64_t rows, int64_t cols, const void* w_post, const void* gate, int64_t ld_gate,

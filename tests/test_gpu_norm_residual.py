@@ -295,7 +295,7 @@ def test_own_workspace_on_another_stream(fp4, monkeypatch):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("eh,ew", [(50, 80), (-40, -90)])
+@pytest.mark.parametrize("eh,ew", [(50, 80), (-40, -90), (-70, -70)])
 def test_stream_and_weight_far_from_one(fp4, dtype, eh, ew):
     """h' w passes binary32 at one end, while y does not."""
     rows, cols = 21, 1000
@@ -390,3 +390,31 @@ def test_parts_of_the_operator_at_model_widths(fp4, dtype, cols):
         check(fp4.norm_residual_backward(None, None, dh_in=dh_in, o=t["o"], rstd_post=f["rstd_post"], **kw),
               oracle.norm_residual_backward(None, None, None, None, wide(dh_in), w["o"], wp, wide(f["rstd_post"]), wg,
                                             per, -2.0))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [130, 4096, 8200])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 2.0 ** -100])
+def test_rows_whose_squares_underflow(fp4, dtype, cols, eps):
+    """Rows of normal numbers whose squares are subnormal or zero in binary32."""
+    exps = np.array([-30, -45, -49, -50, -51, -60, -63, -68, -70, -75, -90, -110, -115])
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn((len(exps), cols), generator=g).double() * torch.from_numpy(2.0 ** exps)[:, None]
+    x = torch.where(x.abs() < 2.0 ** -126, 2.0 ** -126, x).to(dtype)
+    room = torch.zeros((2, len(exps), (cols + 7) // 8 * 8), dtype=dtype, device="cuda")
+    h, o = room[0][:, :cols], room[1][:, :cols]
+    o.copy_(x)
+    w = (1 + 0.2 * torch.randn(cols, generator=g)).to(dtype).cuda()
+    half = half_step(dtype)
+    # before a block
+    f = fp4.norm_residual(o, w_pre=w, eps=eps)
+    ref = oracle.norm_residual(wide(o), w_pre=wide(w), eps=eps)
+    assert_close(f["rstd_pre"], ref["rstd_pre"], 32 * U * ref["rstd_pre"], "rstd_pre")
+    assert_close(f["y"], ref["y"], (40 * U + half) * np.abs(ref["y"]), "y")
+    # after one, onto a stream of zeros, and before the next
+    f = fp4.norm_residual(h, w_pre=w, o=o, w_post=w, eps=eps)
+    ref = oracle.norm_residual(wide(h), wide(o), wide(w), eps=eps)
+    assert_close(f["rstd_post"], ref["rstd_post"], 32 * U * ref["rstd_post"], "rstd_post")
+    assert_close(f["h"], ref["h"], (40 * U + half * (1 + 40 * U)) * np.abs(ref["h"]), "h'")
+    ref2 = oracle.norm_residual(wide(f["h"]), w_pre=wide(w), eps=eps)
+    assert_close(f["rstd_pre"], ref2["rstd_pre"], 32 * U * ref2["rstd_pre"], "rstd_pre")
