@@ -613,7 +613,8 @@ def _gate_of(gate, rows_per_group, rows, cols, dtype, dev):
     if rows_per_group is None or rows_per_group < 1:
         raise ValueError("a gate needs rows_per_group >= 1")
     shape = ((rows + rows_per_group - 1) // rows_per_group, cols)
-    return gate.data_ptr(), _mat(gate, "gate", shape, dtype, dev), rows_per_group
+    # no more than the rows: the library's integers have 64 bits
+    return gate.data_ptr(), _mat(gate, "gate", shape, dtype, dev), min(rows_per_group, max(rows, 1))
 
 
 def _new_vector(t, what: str, shape, like, dev):

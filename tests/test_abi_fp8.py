@@ -186,3 +186,12 @@ def test_sizes_beyond_the_tile_coordinates_are_refused(n):
                                        None, A, A, 8, None, 0, A, None, None, A, 4096, stream=0)
     with pytest.raises(fp4.Fp4Error, match="UNSUPPORTED_SHAPE"):
         fp4.fp4_fp8_block_gemm(A, 128, A, A, 128, A, 1, n, 8, 128, A, fp4.FP4_OUT_F32, 8, stream=0)
+
+
+@pytest.mark.parametrize("per", [5, 2 ** 63, 2 ** 64 + 1, 2 ** 70])
+def test_groups_longer_than_the_rows_reach_the_library_as_one(per):
+    """Python's integers are longer than the library's: 2^64 + 1 must not arrive as 1,
+    which would read a gate row per row behind the only one there is."""
+    address, pitch, got = fp4._gate_of(cpu(1, 104), per, 4, 104, torch.bfloat16, -1)
+    assert got == 4 and pitch == 112
+    assert fp4._gate_of(cpu(0, 104), per, 0, 104, torch.bfloat16, -1)[2] == 1
