@@ -641,11 +641,14 @@ def norm_residual(h, w_pre=None, o=None, w_post=None, gate=None, rows_per_group=
     h' (h itself without o), "rstd_post", "rstd_pre", and with w_pre "y", or
     with quantize=True "q", y as an FP8 tensor of 1 x 128 blocks}.  `out` may
     hold buffers under those names; out["y"] and out["q"] together get both."""
+    out = out or {}
+    if w_pre is None and (quantize or out.get("y") is not None or out.get("q") is not None):
+        raise ValueError("y and q need the norm before the block: w_pre is not given")
     dev = _device_of(h, "h")
     if h.dim() != 2:
         raise ValueError("h must be 2-D, got %s" % (tuple(h.shape),))
     shape = rows, cols = h.shape
-    dt, dtype, out = in_dtype_of(h), h.dtype, out or {}
+    dt, dtype = in_dtype_of(h), h.dtype
     ldh = _mat(h, "h", shape, dtype, dev)
     if o is None:
         if w_pre is None:

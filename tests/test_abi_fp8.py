@@ -195,3 +195,12 @@ def test_groups_longer_than_the_rows_reach_the_library_as_one(per):
     address, pitch, got = fp4._gate_of(cpu(1, 104), per, 4, 104, torch.bfloat16, -1)
     assert got == 4 and pitch == 112
     assert fp4._gate_of(cpu(0, 104), per, 0, 104, torch.bfloat16, -1)[2] == 1
+
+
+def test_outputs_of_a_norm_that_is_not_asked_for_are_refused():
+    """Without w_pre there is no y: a buffer for it would come back unwritten."""
+    h = cpu(4, 128)
+    q = fp4.alloc_fp8_block(4, 128, device="cpu")
+    for kw in (dict(quantize=True), dict(out=dict(y=h)), dict(out=dict(q=q)), dict(quantize=True, out=dict(h=h))):
+        with pytest.raises(ValueError, match="w_pre"):
+            fp4.norm_residual(h, o=h, **kw)
