@@ -3,7 +3,8 @@
 Argument marshalling only: every step of quantization and GEMM runs in the
 library's CUDA kernels.  Pointer arguments take a torch tensor (its
 ``data_ptr()``), an integer address or None; ``stream`` defaults to torch's
-current CUDA stream.  A non-OK status raises :class:`Fp4Error`.
+current CUDA stream, and what a helper allocates comes from the memory of the
+stream that it runs on.  A non-OK status raises :class:`Fp4Error`.
 
 Importing this module loads the library and raises ImportError if it has not
 been built (``python -m fp4_block_scaled_h16_b200.build``): there is no CPU
@@ -12,6 +13,8 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -110,6 +113,27 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on_stream(helper):
+    """Make the helper's `stream` torch's current one for the call.  Memory from
+    another stream's pool may still be in use there, and goes back to that pool
+    while the call on `stream` may not have run yet."""
+    at = list(inspect.signature(helper).parameters).index("stream")
+
+    @functools.wraps(helper)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return helper(*args, **kwargs)
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream))
+        if stream.device_index != torch.cuda.current_device():
+            raise ValueError("stream is on %s, the current device is cuda:%d" % (stream.device, torch.cuda.current_device()))
+        with torch.cuda.stream(stream):
+            return helper(*args, **kwargs)
+    return call
+
+
 def _check(status: int, where: str):
     if status != FP4_OK:
         raise Fp4Error(status, where)
@@ -148,6 +172,7 @@ def fp4_rotate(x, in_dtype, rows, cols, ld, rotation, axis, seed, y, ldy, stream
                            _stream(stream)), "fp4_rotate")
 
 
+@_on_stream
 def rotate(x, rotation, seed=0, out=None, stream=None):
     """The rotation alone along the rows of a 2-D CUDA tensor, in its own dtype (fp4_rotate)."""
     import torch
@@ -165,6 +190,7 @@ def fp4_mxnorm_quantize(x, in_dtype, rows, cols, ld, fmt, rounding, p, c, seed, 
                                     workspace_bytes, _stream(stream)), "fp4_mxnorm_quantize")
 
 
+@_on_stream
 def mxnorm_quantize(x, fmt, p, c, rounding=FP4_RTNE, seed=0, tensor_id=0, out=None, rho=None, workspace=None,
                     stream=None):
     """MXNorm fused with the cast of a 2-D CUDA tensor along its rows
@@ -202,6 +228,7 @@ def fp4_requantize(src_codes, src_scales, src_outer, src_tensor_scale, lines, K,
                                _stream(stream)), "fp4_requantize")
 
 
+@_on_stream
 def requantize(q, fmt, rounding=FP4_RTNE, rotation=FP4_ROT_NONE, double_block=False, seed=0, tensor_id=0,
                tensor_amax=None, out=None, workspace=None, stream=None):
     """Re-quantize the quantized tensor q (lines x K) along the other axis: the
@@ -273,6 +300,7 @@ def alloc_qtensor(lines: int, K: int, fmt: int, double_block: bool = False, devi
         lines=lines, K=K, format=fmt, double_block=bool(double_block))
 
 
+@_on_stream
 def quantize(x, fmt, rounding=FP4_RTNE, rotation=FP4_ROT_NONE, axis=1, double_block=False, seed=0,
              tensor_id=0, tensor_amax=None, out=None, workspace=None, cols=None, stream=None):
     """Quantize a 2-D CUDA tensor (row-major, unit stride in the last dim) into a new or given qtensor."""
@@ -300,6 +328,7 @@ def fp4_quantize_both_axes(x, in_dtype, rows, cols, ld, fmt, rotation, seed, rou
            "fp4_quantize_both_axes")
 
 
+@_on_stream
 def quantize_both_axes(x, fmt, rotation=FP4_ROT_NONE, seed=0, rounding_rows=FP4_RTNE, tensor_id_rows=0,
                        rounding_cols=FP4_RTNE, tensor_id_cols=0, out_rows=None, out_cols=None, workspace=None,
                        stream=None):
@@ -318,6 +347,7 @@ def quantize_both_axes(x, fmt, rotation=FP4_ROT_NONE, seed=0, rounding_rows=FP4_
     return qr, qc
 
 
+@_on_stream
 def gemm(qa, qb, out_dtype=FP4_OUT_F32, out=None, workspace=None, stream=None):
     """C = A B^T on two quantized tensors of the same format (lines along K);
     UFP4 takes a workspace (allocated here when none is given)."""
@@ -365,6 +395,7 @@ def fp4_gemm_outctl(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, a8_codes, 
                                 out_dtype, ldc, _stream(stream)), "fp4_gemm_outctl")
 
 
+@_on_stream
 def channel_amax(x, stream=None):
     """max over rows of |x[:, c]| for a 2-D CUDA tensor (fp4_channel_amax)."""
     import torch
@@ -384,6 +415,7 @@ def outctl_channels(amax, p: float):
     return torch.sort(order).values.to(torch.int32)
 
 
+@_on_stream
 def outctl_quantize(x, channels, k8=None, rounding=FP4_RTNE, rotation=FP4_ROT_NONE, seed=0, tensor_id=0,
                     out=None, stream=None):
     """The OutControl split of a 2-D CUDA tensor along its channels
@@ -404,6 +436,7 @@ def outctl_quantize(x, channels, k8=None, rounding=FP4_RTNE, rotation=FP4_ROT_NO
     return o
 
 
+@_on_stream
 def gemm_outctl(qa, qb, out_dtype=FP4_OUT_F32, out=None, stream=None):
     """C = A B^T on two OutControl-split operands (fp4_gemm_outctl)."""
     import torch
@@ -531,6 +564,7 @@ def _fp8_quantize(x, block_lines, out_rows, out_cols, want_rows, want_cols, stre
     return out_rows, out_cols
 
 
+@_on_stream
 def fp8_block_quantize(x, axis=1, block_lines=1, out=None, stream=None):
     """E4M3 of a 2-D CUDA tensor with a scale per block of 128 along its rows
     (axis 1) or its columns (axis 0: the transposed tensor), of block_lines (1
@@ -543,12 +577,14 @@ def fp8_block_quantize(x, axis=1, block_lines=1, out=None, stream=None):
     raise ValueError("axis must be 0 or 1, got %r" % (axis,))
 
 
+@_on_stream
 def fp8_block_quantize_both_axes(x, block_lines=1, out_rows=None, out_cols=None, stream=None):
     """fp8_block_quantize along the rows and along the columns from one read;
     returns (FP8 tensor of the rows, FP8 tensor of the columns)."""
     return _fp8_quantize(x, block_lines, out_rows, out_cols, True, True, stream)
 
 
+@_on_stream
 def fp8_block_gemm(qa, qb, out_dtype=FP4_OUT_F32, out=None, stream=None):
     """C = A B^T on two FP8 tensors (fp4_fp8_block_gemm): A in 1 x 128 blocks,
     B in 1 x 128 or 128 x 128 blocks."""
@@ -633,6 +669,7 @@ def _new_mat(t, like, shape):
     return torch.empty((shape[0], (shape[1] + 7) // 8 * 8), dtype=like.dtype, device=like.device)[:, :shape[1]]
 
 
+@_on_stream
 def norm_residual(h, w_pre=None, o=None, w_post=None, gate=None, rows_per_group=None, alpha=1.0, eps=1e-6,
                   quantize=False, out=None, stream=None):
     """The norms after and before a block with its gate and the residual update
@@ -684,6 +721,7 @@ def norm_residual(h, w_pre=None, o=None, w_post=None, gate=None, rows_per_group=
     return got
 
 
+@_on_stream
 def norm_residual_backward(dy, h, rstd_pre=None, w_pre=None, dh_in=None, o=None, w_post=None, rstd_post=None,
                            gate=None, rows_per_group=None, alpha=1.0, out=None, workspace=None, stream=None):
     """The gradients of norm_residual (fp4_norm_residual_backward): dy of y, or
@@ -732,8 +770,6 @@ def norm_residual_backward(dy, h, rstd_pre=None, w_pre=None, dh_in=None, o=None,
     if ws_bytes:
         if workspace is None:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=like.device)
-            if stream is not None:       # it returns to the current stream's pool while `stream` may still use it
-                workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), like.device))
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous and on %s" % like.device)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -132,3 +132,65 @@ def test_serving_step_repeats_a_training_rows_result(fp4):
         one = fp4.norm_residual(t["h"][i:i + 1], w_pre=t["w1"], quantize=True)["q"]
         assert torch.equal(one["codes"], whole["codes"][i:i + 1])
         assert torch.equal(fp4.fp8_block_gemm(one, wr, fp4.FP4_OUT_F32), o[i:i + 1])
+
+
+def tensors(r):
+    """Every tensor of a helper's result."""
+    if isinstance(r, torch.Tensor):
+        return [r]
+    return [t for v in (r.values() if isinstance(r, dict) else r) if isinstance(v, (torch.Tensor, dict)) for t in tensors(v)]
+
+
+def calls(fp4):
+    """Helpers that allocate, each as (name, call with a stream)."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((256, 512), generator=g).to(torch.bfloat16).cuda()
+    w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    qa, qb = fp4.fp8_block_quantize(x), fp4.fp8_block_quantize(x, 1, 128)
+    n4, b4 = (fp4.quantize(x, fp4.FP4_NVFP4) for _ in range(2))
+    f = fp4.norm_residual(x, w_pre=w, o=x, w_post=w)
+    return [
+        ("quantize", lambda s: fp4.fp8_block_quantize(x, stream=s)),
+        ("quantize both", lambda s: fp4.fp8_block_quantize_both_axes(x, stream=s)),
+        ("gemm", lambda s: fp4.fp8_block_gemm(qa, qb, stream=s)),
+        ("norm", lambda s: fp4.norm_residual(x, w_pre=w, o=x, w_post=w, stream=s)),
+        ("norm fp8", lambda s: fp4.norm_residual(x, w_pre=w, quantize=True, stream=s)),
+        ("backward", lambda s: fp4.norm_residual_backward(x, f["h"], f["rstd_pre"], w_pre=w, o=x, w_post=w,
+                                                          rstd_post=f["rstd_post"], stream=s)),
+        ("fp4 quantize", lambda s: fp4.quantize(x, fp4.FP4_NVFP4, rotation=fp4.FP4_ROT_H16, stream=s)),
+        ("fp4 gemm", lambda s: fp4.gemm(n4, b4, stream=s)),
+        ("rotate", lambda s: fp4.rotate(x, fp4.FP4_ROT_H16, stream=s)),
+    ]
+
+
+def test_memory_of_another_stream_is_left_alone(fp4):
+    """What a call on a side stream allocates is not memory that the current stream
+    has freed but not finished with, and it is not handed out on the current stream
+    while the side stream has yet to use it."""
+    side = torch.cuda.Stream()
+    for name, call in calls(fp4):
+        want = [v.clone() for v in tensors(call(None))]
+        for stream in (side, side.cuda_stream):
+            torch.cuda.synchronize()
+            sizes = [v.untyped_storage().nbytes() for v in want]
+            old = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+            torch.cuda._sleep(50_000_000)                # tens of milliseconds
+            for t in old:
+                t.fill_(0x7f)                            # still to come when the memory goes back
+            taken = [(t.untyped_storage().data_ptr(), t.numel()) for t in old]
+            del old, t
+            got = call(stream)
+            assert not torch.cuda.current_stream().query()
+            mine = [(v.untyped_storage().data_ptr(), v.untyped_storage().nbytes()) for v in tensors(got)]
+            assert mine
+            assert not [1 for a, n in mine for b, m in taken if a < b + m and b < a + n], name
+            torch.cuda.synchronize()
+            for v, w in zip(tensors(got), want):
+                assert torch.equal(v, w), name
+
+
+def test_stream_of_another_device_is_refused(fp4, monkeypatch):
+    side = torch.cuda.Stream()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 7)
+    with pytest.raises(ValueError, match="stream"):
+        fp4.fp8_block_quantize(torch.zeros((1, 128)), stream=side)
