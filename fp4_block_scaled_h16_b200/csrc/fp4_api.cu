@@ -763,6 +763,7 @@ fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_
     if ((w_pre != nullptr) != (y || codes) || (!o && !w_pre)) return FP4_ERR_INVALID_ARG;
     if (!h || (o && !h_out) || (w_post && !rstd_post) || (w_pre && !rstd_pre) || (codes && !scales))
         return FP4_ERR_INVALID_ARG;
+    if (o && h_out == h && ld_hout != ldh && rows > 1) return FP4_ERR_INVALID_ARG;     // rows over other rows
     const int64_t es = dtype == FP4_IN_BF16 ? 2 : 4;
     fp4_status_t st = check_matrix(h, ldh, cols, es);
     if (st == FP4_OK && o) st = check_matrix(o, ldo, cols, es);
@@ -835,6 +836,7 @@ fp4_status_t fp4_norm_residual_backward(const void* dy, int64_t lddy, const void
     if ((w_pre != nullptr) != (dy != nullptr) || (w_pre && (!h || !rstd_pre)) || (!dy && !dh_in) || !dh)
         return FP4_ERR_INVALID_ARG;
     if ((o != nullptr) != (d_o != nullptr) || (w_post && !rstd_post)) return FP4_ERR_INVALID_ARG;
+    if (dh == dh_in && ld_dh != ld_dhin && rows > 1) return FP4_ERR_INVALID_ARG;       // rows over other rows
     const int64_t es = dtype == FP4_IN_BF16 ? 2 : 4;
     st = check_matrix(dh, ld_dh, cols, es);
     if (st == FP4_OK && dy) st = check_matrix(dy, lddy, cols, es);

@@ -567,7 +567,7 @@ fp4_status_t fp4_norm_residual(const void* o, int64_t ldo, const void* h, int64_
  *   o, ldo, d_o, ld_do   together, or both NULL (no residual update)
  *   w_post, rstd_post, dw_post   together, or all NULL
  *   gate, ld_gate, rows_per_group, dgate   together, or NULL
- *   dh, ld_dh       [rows, ld_dh]; may be dh_in itself
+ *   dh, ld_dh       [rows, ld_dh]; may be dh_in itself (dh == dh_in and ld_dh == ld_dhin)
  *   dw_pre, dw_post   float [cols], overwritten
  *   dgate           float [ceil(rows / rows_per_group), cols], overwritten
  *   workspace       fp4_norm_residual_backward_workspace_size() bytes, 16-byte

@@ -204,3 +204,12 @@ def test_outputs_of_a_norm_that_is_not_asked_for_are_refused():
     for kw in (dict(quantize=True), dict(out=dict(y=h)), dict(out=dict(q=q)), dict(quantize=True, out=dict(h=h))):
         with pytest.raises(ValueError, match="w_pre"):
             fp4.norm_residual(h, o=h, **kw)
+
+
+@no_gpu
+def test_in_place_with_another_pitch_is_refused():
+    """Rows would be written over rows that are still to be read."""
+    assert n(ldho=112) == n(ldh=112) == INVALID
+    assert n(ldho=112, rows=1) == n(ldho=112, h_out=2 * A) == NO_DEVICE
+    assert b(lddh=112) == b(lddhi=112) == INVALID
+    assert b(lddh=112, rows=1) == b(lddh=112, dh=2 * A) == NO_DEVICE
