@@ -285,3 +285,29 @@ def test_gemm_with_scales_far_apart(fp4, M, N, K, b_lines, ea, eb):
         assert torch.isfinite(C).all()
         assert_within_gemm_bound(C.cpu().numpy(), C64, bound, False, "%s" % ((M, N, K, b_lines, ea, eb, pairs),))
     assert fp4.fp4_last_error() == fp4.FP4_OK
+
+
+@pytest.mark.parametrize("M,N,K,b_lines", [(2300, 1900, 640, 1), (2300, 1900, 640, 128), (333, 1000, 1300, 128),
+                                           (300, 1000, 1300, 1), (50, 700, 2050, 128), (9, 700, 2050, 1)])
+def test_gemm_rows_and_columns_do_not_see_each_other(fp4, M, N, K, b_lines):
+    """With other tokens around it a token keeps its row, bit for bit, and a line of the weight its column."""
+    g = torch.Generator().manual_seed(M)
+    x, w = torch.randn((M, K), generator=g), torch.randn((N, K), generator=g)
+    C = fp4.fp8_block_gemm(fp4.fp8_block_quantize(padded(x)), fp4.fp8_block_quantize(padded(w), 1, b_lines))
+    rows = [0, M // 2, M - 1]
+    x2 = torch.randn((M, K), generator=g) * 100
+    x2[rows] = x[rows]
+    D = fp4.fp8_block_gemm(fp4.fp8_block_quantize(padded(x2)), fp4.fp8_block_quantize(padded(w), 1, b_lines))
+    assert torch.equal(C[rows], D[rows]) and not torch.equal(C, D)
+    block = slice(128, 256) if b_lines == 128 else slice(130, 131)       # lines that share a scale
+    w2 = torch.randn((N, K), generator=g) * 100
+    w2[block] = w[block]
+    D = fp4.fp8_block_gemm(fp4.fp8_block_quantize(padded(x)), fp4.fp8_block_quantize(padded(w2), 1, b_lines))
+    assert torch.equal(C[:, block], D[:, block]) and not torch.equal(C, D)
+
+
+def padded(t):
+    """On the GPU in fp32, with a row pitch of a multiple of 16 bytes."""
+    room = torch.zeros((t.shape[0], (t.shape[1] + 3) // 4 * 4), device="cuda")
+    room[:, :t.shape[1]] = t.cuda()
+    return room[:, :t.shape[1]]
