@@ -25,8 +25,9 @@
 // products below.  One thread needs about 800 cycles for a chunk's two waits, four
 // MMAs and two commits beside a busy promotion, so two issuers take turns.  With
 // 1 x 128 blocks of B the promotion's product per element more makes it 1040.
-// QKV Fprop 8192 x 6144 x 4096: 193 us, 2140 TFLOP/s (0.64 of twice the bf16
-// burst rate); Wgrad 4096 x 14336 x 8192 in f32: 563 us, 1710 TFLOP/s.
+// QKV Fprop 8192 x 6144 x 4096: 196 us, 2100 TFLOP/s (0.63 of twice the bf16
+// burst rate); Wgrad 4096 x 14336 x 8192 in f32: 584 us, 1650 TFLOP/s (570 to 632
+// from run to run, by the clocks that the power limit leaves).
 //
 // Roles (both CTAs, 384 threads, persistent over pair tiles, one CTA per SM):
 //   warp 0   TMA producer: this CTA's 128 rows of A and 128 lines of B per
@@ -65,7 +66,8 @@ constexpr int COLS = PN / (PROMO_WARPS / 4);         // columns of the tile per 
 constexpr int STAGES = 5;
 // Ring of scale slots, without barriers of its own: a stage is refilled once its
 // MMAs are done; those were issued once the promotion had read the partial two
-// chunks before, and so was past the scales of the chunk before that one.
+// chunks before, and so was past the scales of the chunk before that one (their
+// values are in its sums by then: mbar_arrive_cluster_relaxed).
 constexpr int SC_SLOTS = 8;
 static_assert(SC_SLOTS >= STAGES + 3, "scales are read before their slot is refilled");
 constexpr uint32_t A_BYTES = 128 * BK, B_BYTES = 128 * BK;

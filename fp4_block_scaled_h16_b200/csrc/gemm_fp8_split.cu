@@ -16,9 +16,10 @@
 // in rank order through distributed shared memory, so the result does not
 // depend on timing and no workspace or second launch is needed.
 //
-// One token, N = 6144, K = 4096: 7.25 us, 25 MB of weights at 3470 GB/s; about
+// One token, N = 6144, K = 4096: 9.2 us, 25 MB of weights out of HBM at 2750 GB/s,
+// and 7.5 us where they lie in L2 (as in the comparisons at the kernel); about
 // half of it is the launch, the first loads' latency and the sum over the
-// cluster.  333 x 4096 x 14336: 32.7 us, 1200 TFLOP/s, on 48 clusters of two (the
+// cluster.  333 x 4096 x 14336: 33 us, 1190 TFLOP/s, on 48 clusters of two (the
 // GPU holds 45 of three).  A chunk takes 0.42 us there, of which the loads alone
 // would take 0.33 (264 MB out of L2 for all tiles, 14 TB/s) and the MMAs alone
 // 0.28; 9 us are the launch, the first loads and the sum over the cluster, 2.6 of
@@ -67,7 +68,8 @@ struct SCfg {
     static constexpr int PBUF = WIDE ? 2 : 4;             // TMEM buffers of NT columns
     // Scales have a longer ring, without barriers of its own, so that a stage is
     // free when its MMAs are done: they were issued once the promotion had read the
-    // partial PBUF chunks before, and so was past the scales of the chunk before that.
+    // partial PBUF chunks before, and so was past the scales of the chunk before that
+    // (their values are in its sums by then: mbar_arrive_cluster_relaxed).
     static constexpr int STAGES =
         (int)((232448u / CTAS - 1024u - EXTRA - (PBUF + 1) * SC_BYTES) / (STAGE_BYTES + SC_BYTES));
     static constexpr int SC_SLOTS = STAGES + PBUF + 1;
@@ -492,7 +494,7 @@ cudaError_t run_nt(const Fp8GemmArgs& g, cudaStream_t s) {
 
 // With 1 x 128 blocks of B the promotion, one product per element more, bounds a
 // chunk, not its loads, so tiles of 192 lines gain where they spread over more SMs:
-// 333 x 4096 x 14336 44.1 -> 37.6 us, 512 x 6144 x 4096 28.0 -> 24.3, but 300 x
+// 333 x 4096 x 14336 44.1 -> 36.2 us, 512 x 6144 x 4096 28.0 -> 23.3, but 300 x
 // 6144 x 4096 20.2 -> 23.8 where they leave no room to split K.  (With 128 x 128
 // blocks they load more for the same product: 33.2 -> 36.3 us for the first.)
 template <bool OUT_BF16>

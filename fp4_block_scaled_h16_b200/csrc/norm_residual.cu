@@ -26,11 +26,11 @@
 // rounded before its norm, because the stored h' is what the next block and the
 // backward call see.
 //
-// 8192 x 4096 in bf16, both weights and a gate: forward 48 us (5600 GB/s; 44 us
-// without a gate), backward with its sums 75 us (5370 GB/s); without w_post, FP8
-// codes for y, 42 us (5650 GB/s).  What
+// 8192 x 4096 in bf16, both weights and a gate: forward 50 us (5400 GB/s; 46 us
+// without a gate), backward with its sums 76 us (5310 GB/s); without w_post, FP8
+// codes for y, 44 us (5370 GB/s).  What
 // is left to the copy rate is the block sums' barrier between a row's loads and its
-// stores, and in the backward call the arithmetic of the three sums.  One row 3.3
+// stores, and in the backward call the arithmetic of the three sums.  One row 3.6
 // us; a backward call adds a second launch, 6 us at least.
 #include <type_traits>
 
@@ -802,25 +802,29 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormBwdArgs a, i
 
 // vectors per thread and threads for a row of `cols` elements.  Two vectors per
 // thread up to 4096 columns leave registers for three CTAs of 256 threads per SM:
-// norm 8192 x 4096 52.9 us, against 67.6 with one vector and 512 threads, 58.9
-// with two CTAs per SM and 66.4 with four, which spill.
+// norm 8192 x 4096 52.9 us at the time, against 67.6 with one vector and 512
+// threads, 58.9 with two CTAs per SM and 66.4 with four, which spill.
 void shape_of(int64_t cols, int& vpt, int& threads) {
     const int64_t nvec = (cols + VEC - 1) / VEC;
     vpt = nvec <= 256 ? 1 : (nvec <= 1024 ? 2 : 4);
     threads = (int)(((nvec + vpt - 1) / vpt + 31) / 32 * 32);
 }
 
-// CTAs of the backward kernel, which have a line of partial sums each: as many as a
-// B200 holds at once, three per SM with up to 256 threads of one vector, two with
-// two, one beyond 4096 columns (4364 x 2034 47 us at the time, 57 with two).  Rows of up
-// to 1024 columns have a form of 128 threads with all their registers and take 512
-// threads per SM: with 768 the longer sum over the lines costs more than the rows
-// gain (1031 x 1003 12.2 us against 14.1).
+// CTAs of the backward kernel, which have a line of partial sums each: three per SM
+// with up to 256 threads of one vector, two with two, one beyond 4096 columns, as
+// many as the SM holds at once (4364 x 2034 47 us at the time, 57 with two).  Rows
+// of up to 1024 columns have a form of 128 threads with all their registers and
+// take up to 512 threads per SM: 16, 8, 4 and 4 CTAs of 32, 64, 96 and 128.  The SM
+// would hold more, but with 768 threads the longer sum over the lines costs more
+// than the rows gain (1031 x 1003 12.2 us against 14.1).  The SMs are a B200's and
+// not asked for, so that the workspace's size and the order of the sums follow from
+// the sizes alone.
+constexpr int64_t BWD_SMS = 148;
 int64_t norm_bwd_limit(int64_t cols) {
     int vpt, threads;
     shape_of(cols, vpt, threads);
-    if (threads > 256) return 148;
-    return vpt == 1 && threads > 128 ? 444 : 296 * (256 / threads);
+    if (threads > 256) return BWD_SMS;
+    return vpt == 1 && threads > 128 ? 3 * BWD_SMS : 2 * BWD_SMS * (256 / threads);
 }
 int64_t norm_bwd_ctas(const NormBwdArgs& a) {
     const int64_t limit = norm_bwd_limit(a.cols);

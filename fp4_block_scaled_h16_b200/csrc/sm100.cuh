@@ -271,7 +271,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
 
 // the same without ordering this thread's memory accesses: for a hand-over of
 // TMEM, which tcgen05.fence orders (a release at cluster scope waits for every
-// access of the thread, over a microsecond in a promotion loop)
+// access of the thread, over a microsecond in a promotion loop).  It does not order
+// reads of shared memory, such as those of scales beside a TMEM buffer.  A ring of
+// them may rest on it all the same if a slot is only written again behind the
+// reading warp's arrive for the chunk after: by then the values read have gone into
+// sums with the chunk's TMEM values, whose registers the next chunk's load has taken.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t caddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
